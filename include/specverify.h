@@ -41,6 +41,15 @@
  *                 distribution P(j) of accepted lengths is the statistic a
  *                 prefetcher plans with; the histogram is that distribution.
  *
+ *  sv_tree_attention, sv_verify_tree, sv_cache_append, sv_cache_commit,
+ *  sv_cache_fork, sv_cache_resize -- the same verification for a TREE of
+ *                 drafted tokens (several candidates after one token) around
+ *                 a paged key/value cache: attention of the tree's rows, the
+ *                 lossless walk, the accepted branch moved to the front of
+ *                 the cache, and the cache's pages.  No passage of the pages
+ *                 defines them; they extend the rule of sv_verify, which they
+ *                 equal on a chain.
+ *
  *  sv_vat_loss -- the same page and sections, with the end of section
  *                 "第二件事，改权重分配的锚点": the drafter's training loss
  *                 combines soft-label distillation from the target's output
@@ -125,7 +134,7 @@
 extern "C" {
 #endif
 
-#define SV_ABI_VERSION 7
+#define SV_ABI_VERSION 8
 #define SV_MAX_DRAFT 64 /* k is limited to one 64-lane wavefront */
 #define SV_MAX_DRAFT_CHOICES 8
 
@@ -145,10 +154,14 @@ typedef enum sv_status {
     SV_ERR_BAD_CONTROL = 10,      /* draft-length controller thresholds out of range */
     SV_ERR_MISALIGNED = 11,       /* an array that must be 16-byte aligned is not */
     SV_ERR_CAPTURING = 12,        /* a tagged call on a stream that is being captured into a graph */
-    SV_ERR_SCRATCH_TOO_SMALL = 13 /* sv_verify_noalloc: the call needs more than SV_NOALLOC_SCRATCH_BYTES */
+    SV_ERR_SCRATCH_TOO_SMALL = 13, /* sv_verify_noalloc: the call needs more than SV_NOALLOC_SCRATCH_BYTES */
+    SV_ERR_BAD_SCALE = 14,        /* attention scale not finite and > 0 */
+    SV_ERR_ALIASED = 15           /* two arrays that must be distinct are the same */
 } sv_status;
 
-typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+/* SV_F16 (IEEE binary16) is a type of the key/value cache and the attention
+ * over it; logits are SV_F32 or SV_BF16. */
+typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype;
 
 typedef enum sv_draft_kind { SV_DRAFT_LOGITS = 0, SV_DRAFT_ONEHOT = 1 } sv_draft_kind;
 
@@ -511,6 +524,247 @@ sv_status sv_draft_len_init(sv_draft_len_ctl* ctl, const int32_t* choices, int32
  * changes nothing.  Errors: SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE (k is not the
  * current choice). */
 sv_status sv_draft_len_update(sv_draft_len_ctl* ctl, const int32_t* hist, int32_t k, int32_t* next_k);
+
+/*
+ * ---- Trees of drafted tokens ------------------------------------------------
+ *
+ * A tree has k draft nodes under the root, the last committed token (whose
+ * key and value are not in the cache yet).  parents[b][i] is the parent of
+ * node i: an earlier node (< i), -1 for a child of the root, or -2 where node i
+ * is absent (trees of one batch may differ in size).  Row 0 of a sequence's
+ * queries, logits and new cache rows is the root's, row 1 + i node i's; a chain
+ * has parents[b][i] = i - 1 and the rows of sv_verify.
+ *
+ * The cache: k_cache and v_cache [layer][page][kv_head][page_size][head_dim].
+ * page_table[b][s] is the page of positions s * page_size onward of sequence
+ * b, -1 where it has none.  seq_len[b] counts the committed positions; a
+ * tree's rows stand behind them, the root at position seq_len[b], node i at
+ * seq_len[b] + 1 + i.  A negative seq_len marks an absent sequence.
+ *
+ * These entry points may be captured into a HIP graph: lengths, trees and
+ * page tables are read on the device at each replay.
+ */
+
+/* Shape and options of one sv_tree_attention call (one layer). */
+typedef struct sv_tree_attention_desc {
+    int32_t B;            /* sequences, in [0, 65535] */
+    int32_t k;            /* draft nodes, in [0, 64]; 0: the root alone (plain decoding) */
+    int32_t q_heads;      /* a multiple of kv_heads, at most 1024 */
+    int32_t kv_heads;     /* >= 1 */
+    int32_t head_dim;     /* 64, 96, 128 or 256 */
+    int32_t n_pages;      /* pages of the cache; n_pages * kv_heads * page_size < 2^32 */
+    int32_t page_size;    /* a power of two in [1, 1024] */
+    int32_t max_pages;    /* columns of page_table; max_pages * page_size <= 2^30 */
+    sv_dtype dtype;       /* SV_BF16 or SV_F16: queries, cache and output */
+    float scale;          /* of the scores, finite and > 0 */
+    int64_t q_stride_b;   /* strides of q in elements, >= 0 and multiples of 8 */
+    int64_t q_stride_r;
+    int64_t q_stride_h;
+} sv_tree_attention_desc;
+
+/* Workspace bytes sv_tree_attention needs for `desc` (0: NULL or invalid). */
+size_t sv_tree_attention_workspace_bytes(const sv_tree_attention_desc* desc);
+
+/*
+ * Attention of a tree's rows over the cache: row r of sequence b attends to
+ * the committed positions, the root, its ancestors and itself,
+ *   out = sum_j e^{s_j} v_j / sum_j e^{s_j},  s_j = scale q . k_j.
+ *
+ *  q              device, [B][k+1][q_heads][head_dim] by the strides, 16-byte
+ *                 aligned; query head h reads key head h / (q_heads / kv_heads)
+ *  k_cache, v_cache  device, one layer, [n_pages][kv_heads][page_size]
+ *                 [head_dim], 16-byte aligned; the tree's rows already appended
+ *  page_table     device, [B][max_pages] int32
+ *  seq_len        device, [B] int32
+ *  parents        device, [B][k] int32 (may be NULL when k == 0)
+ *  out            device out, [B][k+1][q_heads][head_dim] dtype, 16-byte aligned
+ *  lse_out        device out or NULL, [B][k+1][q_heads] float32: ln sum e^{s_j}
+ *  workspace      device, >= sv_tree_attention_workspace_bytes(desc) bytes,
+ *                 16-byte aligned (needs no clearing).  Calls that use the same
+ *                 workspace must not overlap in time.
+ *
+ * Rows that see nothing (absent nodes: parent -2, out of [-2, i) or absent
+ * itself; absent sequences, and those with seq_len + k + 1 > max_pages *
+ * page_size) get out 0 and lse -inf.  What the cache holds where a row does
+ * not attend (NaN and infinities included) does not reach it.  A page number
+ * outside [0, n_pages) under a position that is attended gives an unspecified
+ * (but in-bounds) result.  Scores, sums and maxima are 32-bit; the softmax
+ * weights are rounded to dtype for the matrix product.
+ * Errors (nothing launched): SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE,
+ * SV_ERR_BAD_DTYPE, SV_ERR_BAD_SCALE, SV_ERR_MISALIGNED,
+ * SV_ERR_WORKSPACE_TOO_SMALL.  Launch failure: SV_ERR_HIP.
+ */
+sv_status sv_tree_attention(const sv_tree_attention_desc* desc, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* page_table, const int32_t* seq_len,
+                            const int32_t* parents, void* out, float* lse_out, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* Shape and options of one sv_verify_tree call. */
+typedef struct sv_verify_tree_desc {
+    int32_t B;                 /* sequences, >= 0 */
+    int32_t k;                 /* draft nodes per sequence, in [1, 64] */
+    int32_t V;                 /* vocabulary size, in [1, 2^24] */
+    int32_t draft_rows;        /* rows of draft_logits per sequence, in [1, k+1]; unused (any value) without them */
+    sv_dtype dtype;            /* of both logit arrays, SV_F32 or SV_BF16 */
+    sv_draft_kind draft_kind;  /* children drawn from draft logits, or proposed without a distribution */
+    float temperature;         /* T: 0 (greedy) or finite >= 1e-4 */
+} sv_verify_tree_desc;
+
+/* Workspace bytes sv_verify_tree needs for `desc` (0: NULL or invalid). */
+size_t sv_verify_tree_workspace_bytes(const sv_verify_tree_desc* desc);
+
+/*
+ * Lossless verification of a tree.  From the root, the children of the
+ * current node are tested in index order with p = softmax(its target row / T);
+ * the first one kept becomes the current node; where none is kept (or there is
+ * none) the target supplies one token.
+ *  - SV_DRAFT_LOGITS: the children are independent draws from q =
+ *    softmax(the node's draft row / T).  Each is kept with probability
+ *    min(1, r(x)/q(x)), r = p for the first and norm(max(0, r - q)) after each
+ *    rejection: u * q(x) < r(x).  The token is drawn from r.
+ *  - SV_DRAFT_ONEHOT: child x is kept with what p gives it once the rejected
+ *    siblings' tokens are removed: u * (1 - sum p(rejected)) < p(x); a token
+ *    proposed again is not kept.  The token is drawn from p without them.
+ *  - T == 0: the child whose token is the target's lowest argmax is kept (the
+ *    first of equal ones); the token is that argmax.
+ * Draws invert the cumulative weight in ascending token id with
+ * uniforms[b][k], tests use uniforms[b][i].  The committed tokens are
+ * distributed as samples of the target alone; a chain gives sv_verify's result.
+ *
+ *  target_logits  device, [B][k+1][V] dtype: row 0 after the root, row 1+i after
+ *                 node i.  Only rows on the walked path are read.
+ *  draft_logits   device, [B][draft_rows][V] dtype: row 0 what the root's
+ *                 children were drawn from, row 1+i node i's; every node with
+ *                 children needs its row (leaves do not).  Unused (may be NULL)
+ *                 for SV_DRAFT_ONEHOT or T == 0.
+ *  draft_tokens   device, [B][k] int32, in [0, V) where the node is present
+ *  parents        device, [B][k] int32
+ *  uniforms       device, [B][k+1] float32 in [0,1) (unused at T == 0)
+ *  accepted_len   device out, [B] int32: nodes kept, -1 for a refused tree (a
+ *                 parent outside [-2, i), a child of an absent node, a token
+ *                 outside [0, V), a node with children but no draft row)
+ *  out_tokens     device out, [B][k+1] int32: the kept nodes' tokens, the
+ *                 target's token, then -1 (all -1 for a refused tree)
+ *  path_out       device out, [B][k] int32: the kept nodes, then -1
+ *  workspace      device, >= sv_verify_tree_workspace_bytes(desc) bytes, 64-byte
+ *                 aligned, zero-filled once before first use; every call that
+ *                 returns SV_OK leaves it ready for the next.  Not shared with
+ *                 other entry points; calls that use the same workspace must
+ *                 not overlap in time.
+ *
+ * Probabilities and sums are 64-bit.  NaN logits and rows that are all -inf
+ * give unspecified (but in-bounds) results.
+ * Errors (nothing launched): SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE,
+ * SV_ERR_BAD_DTYPE, SV_ERR_BAD_TEMPERATURE, SV_ERR_BAD_DRAFT_KIND,
+ * SV_ERR_MISALIGNED, SV_ERR_WORKSPACE_TOO_SMALL.  Launch failure: SV_ERR_HIP.
+ */
+sv_status sv_verify_tree(const sv_verify_tree_desc* desc, const void* target_logits, const void* draft_logits,
+                         const int32_t* draft_tokens, const int32_t* parents, const float* uniforms,
+                         int32_t* accepted_len, int32_t* out_tokens, int32_t* path_out, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* A paged cache.  Pages are referred to by page_table rows and counted in
+ * page_refs (device, [n_pages] int32): a page is free when its count is 0. */
+typedef struct sv_cache_desc {
+    int32_t n_seqs;       /* sequences (rows of page_table), in [0, 4096] */
+    int32_t n_pages;      /* >= 1 */
+    int32_t page_size;    /* a power of two in [1, 1024] */
+    int32_t max_pages;    /* columns of page_table, >= 1; max_pages * page_size <= 2^30 */
+    int32_t n_layers;     /* >= 1 */
+    int32_t kv_heads;     /* in [1, 1024] */
+    int32_t head_dim;     /* a multiple of 8 in [8, 1024] */
+    sv_dtype dtype;       /* SV_BF16 or SV_F16 */
+} sv_cache_desc;
+
+/* Strides of the new rows of sv_cache_append, in elements, >= 0 and multiples of 8. */
+typedef struct sv_cache_rows {
+    int32_t t;            /* rows per sequence, >= 0 */
+    int64_t k_stride_b, k_stride_t, k_stride_h;
+    int64_t v_stride_b, v_stride_t, v_stride_h;
+} sv_cache_rows;
+
+/*
+ * Writes new keys and values behind the sequences' committed positions, in
+ * one layer (desc->n_layers is not used).  Row j < count[b] goes to position
+ * seq_len[b] + j; seq_len is not changed, so that every layer is written alike.
+ *
+ *  k_new, v_new   device, [n_seqs][t][kv_heads][head_dim] by the strides, 16-byte aligned
+ *  count          device, [n_seqs] int32 or NULL (t rows each); taken into [0, t]
+ *  page_table     device, [n_seqs][max_pages] int32
+ *  seq_len        device, [n_seqs] int32 (negative: nothing is written)
+ *  k_cache, v_cache  device in/out, one layer, 16-byte aligned; distinct
+ *
+ * Rows whose position has no page (past the table, page number outside
+ * [0, n_pages)) are dropped.  Pages shared by several sequences must not be
+ * written: sv_cache_fork leaves every sequence's last page its own.
+ * Errors: SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE, SV_ERR_BAD_DTYPE,
+ * SV_ERR_MISALIGNED, SV_ERR_ALIASED (k_cache == v_cache), SV_ERR_HIP.
+ */
+sv_status sv_cache_append(const sv_cache_desc* desc, const sv_cache_rows* rows, const void* k_new, const void* v_new,
+                          const int32_t* count, const int32_t* page_table, const int32_t* seq_len, void* k_cache,
+                          void* v_cache, hipStream_t stream);
+
+/*
+ * Commits an accepted branch: in every layer the rows of the nodes path[b][0],
+ * path[b][1], ... move to the first positions behind the root, in place, and
+ * new_len[b] = seq_len[b] + 1 + accepted_len[b].
+ *
+ *  path, accepted_len  device, [n_seqs][k] and [n_seqs] int32 as sv_verify_tree wrote them
+ *  k              draft nodes, in [1, 64]
+ *  seq_len        device, [n_seqs] int32
+ *  new_len        device out, [n_seqs] int32; not seq_len (other workgroups still read it)
+ *  k_cache, v_cache  device in/out, [n_layers]..., 16-byte aligned; distinct
+ *
+ * A sequence with accepted_len outside [0, k], a path that is not increasing
+ * in [j, k), or seq_len < 0 keeps its rows and its length.
+ * Errors: SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE, SV_ERR_BAD_DTYPE,
+ * SV_ERR_MISALIGNED, SV_ERR_ALIASED (new_len == seq_len, k_cache == v_cache),
+ * SV_ERR_HIP.
+ */
+sv_status sv_cache_commit(const sv_cache_desc* desc, int32_t k, const int32_t* path, const int32_t* accepted_len,
+                          const int32_t* page_table, const int32_t* seq_len, int32_t* new_len, void* k_cache,
+                          void* v_cache, hipStream_t stream);
+
+/* Workspace bytes sv_cache_fork needs for n pairs (0: desc NULL or invalid, or n out of range). */
+size_t sv_cache_fork_workspace_bytes(const sv_cache_desc* desc, int32_t n);
+
+/*
+ * Forks sequences: dst[i] becomes a continuation of src[i] with the same
+ * length.  Whole pages are shared (their counts rise), a begun last page is
+ * copied, in every layer, to the lowest free page.
+ *
+ *  n              pairs, in [0, 4096]
+ *  src, dst       device, [n] int32; dst rows must be empty (page_count 0)
+ *  page_table, page_count, page_refs, seq_len  device in/out, [n_seqs][max_pages], [n_seqs],
+ *                 [n_pages], [n_seqs] int32
+ *  status         device out or NULL, [n] int32: 1 done; 0 refused: an index out of
+ *                 range, dst not empty or named by an earlier pair, src named as a
+ *                 destination, src with more positions than pages, or no free page
+ *                 left (free pages go to the pairs in order)
+ *  workspace      device, >= sv_cache_fork_workspace_bytes(desc, n) bytes (needs no clearing)
+ * Errors: SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE, SV_ERR_BAD_DTYPE,
+ * SV_ERR_MISALIGNED, SV_ERR_ALIASED (k_cache == v_cache),
+ * SV_ERR_WORKSPACE_TOO_SMALL, SV_ERR_HIP.
+ */
+sv_status sv_cache_fork(const sv_cache_desc* desc, int32_t n, const int32_t* src, const int32_t* dst,
+                        int32_t* page_table, int32_t* page_count, int32_t* page_refs, int32_t* seq_len,
+                        void* k_cache, void* v_cache, int32_t* status, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/*
+ * Gives every sequence the pages for want_len[b] positions (want_len < 0: as it
+ * is; 0 frees all): pages behind the new end lose a reference and leave the
+ * table, missing ones are taken from the free pages, lowest number first, in
+ * order of b.  Pages freed by this call can be given out by it.  seq_len is the
+ * caller's.
+ *
+ *  status         device out or NULL, [n_seqs] int32: 1 done; 0 unchanged: want_len (or
+ *                 page_count) beyond the table, or the free pages ran out before its
+ *                 wish was complete (then the later growing sequences are refused too)
+ * Errors: SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE, SV_ERR_BAD_DTYPE, SV_ERR_HIP.
+ */
+sv_status sv_cache_resize(const sv_cache_desc* desc, const int32_t* want_len, int32_t* page_table,
+                          int32_t* page_count, int32_t* page_refs, int32_t* status, hipStream_t stream);
 
 /*
  * Speed-of-light references (measurement only; no passage of the pages

@@ -12,7 +12,8 @@ Names follow the C ABI in ``include/specverify.h``: ``sv_verify`` (and
 ``sv_verify_ex`` when row statistics or a probe are asked for) ->
 :func:`verify`, ``sv_vat_labels`` (``sv_vat_labels_ex``) -> :func:`vat_labels`, ``sv_vat_loss`` ->
 :func:`vat_loss`, ``sv_verify_lm_head_greedy`` -> :func:`verify_lm_head_greedy`,
-``sv_verify_lm_head`` -> :func:`verify_lm_head`.
+``sv_verify_lm_head`` -> :func:`verify_lm_head`.  Trees of drafted tokens and the paged cache (``sv_tree_attention``, ``sv_verify_tree``,
+``sv_cache_*``) are in :mod:`.tree` and reached from here.
 """
 from __future__ import annotations
 
@@ -23,7 +24,8 @@ from typing import NamedTuple, Optional
 __all__ = ["verify", "verify_noalloc", "vat_labels", "vat_loss", "verify_lm_head_greedy", "verify_lm_head", "accept_histogram",
            "Verifier", "VatLabeler", "VatLoss", "LmHeadVerifier", "LmHeadSampler",
            "DraftLengthController", "SVError", "library_path", "load_library", "SV_F32", "SV_BF16", "SV_DRAFT_LOGITS",
-           "SV_DRAFT_ONEHOT", "STATUS"]
+           "SV_DRAFT_ONEHOT", "STATUS", "tree_attention", "TreeAttention", "verify_tree", "TreeVerifier",
+           "cache_append", "cache_commit", "cache_fork", "cache_resize", "SV_F16"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libspecverify.so")
@@ -33,7 +35,8 @@ SV_DRAFT_LOGITS, SV_DRAFT_ONEHOT = 0, 1
 STATUS = {0: "SV_OK", 1: "SV_ERR_NULL_ARG", 2: "SV_ERR_BAD_SHAPE", 3: "SV_ERR_BAD_DTYPE",
           4: "SV_ERR_BAD_TEMPERATURE", 5: "SV_ERR_WORKSPACE_TOO_SMALL", 6: "SV_ERR_HIP",
           7: "SV_ERR_BAD_DRAFT_KIND", 8: "SV_ERR_BAD_DECAY", 9: "SV_ERR_BAD_HARD_WEIGHT", 10: "SV_ERR_BAD_CONTROL",
-          11: "SV_ERR_MISALIGNED", 12: "SV_ERR_CAPTURING", 13: "SV_ERR_SCRATCH_TOO_SMALL"}
+          11: "SV_ERR_MISALIGNED", 12: "SV_ERR_CAPTURING", 13: "SV_ERR_SCRATCH_TOO_SMALL", 14: "SV_ERR_BAD_SCALE",
+          15: "SV_ERR_ALIASED"}
 STATUS_CODE = {name: code for code, name in STATUS.items()}
 
 EXPORTED_SYMBOLS = ("sv_abi_version", "sv_status_str", "sv_verify_workspace_bytes", "sv_verify", "sv_verify_ex",
@@ -42,7 +45,10 @@ EXPORTED_SYMBOLS = ("sv_abi_version", "sv_status_str", "sv_verify_workspace_byte
                     "sv_vat_loss", "sv_vat_loss_grad",
                     "sv_lm_head_workspace_bytes", "sv_verify_lm_head_greedy", "sv_lm_head_sample_workspace_bytes",
                     "sv_verify_lm_head", "sv_accept_histogram",
-                    "sv_draft_len_init", "sv_draft_len_update", "sv_sol_read", "sv_sol_read_write")
+                    "sv_draft_len_init", "sv_draft_len_update", "sv_sol_read", "sv_sol_read_write",
+                    "sv_tree_attention_workspace_bytes", "sv_tree_attention", "sv_verify_tree_workspace_bytes",
+                    "sv_verify_tree", "sv_cache_append", "sv_cache_commit", "sv_cache_fork_workspace_bytes",
+                    "sv_cache_fork", "sv_cache_resize")
 
 
 class SVError(RuntimeError):
@@ -155,6 +161,7 @@ def load_library():
     lib.sv_sol_read.argtypes = [vp, sz, vp, vp]
     lib.sv_sol_read_write.restype = ctypes.c_int
     lib.sv_sol_read_write.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_int, vp]
+    _tree.bind(lib)
     _lib = lib
     return lib
 
@@ -783,3 +790,8 @@ class DraftLengthController:
         if st:
             raise SVError(st, "sv_draft_len_update", self._lib)
         return int(nxt.value)
+
+
+from . import tree as _tree  # noqa: E402  (uses the helpers above)
+from .tree import (SV_F16, TreeAttention, TreeVerifier, cache_append, cache_commit, cache_fork,  # noqa: E402
+                   cache_resize, tree_attention, verify_tree)

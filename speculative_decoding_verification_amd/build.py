@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -40,6 +41,9 @@ def build(verbose: bool = False) -> str:
         c_obj = os.path.join(tmp, "sv_control.o")
         l_obj = os.path.join(tmp, "sv_lmhead.o")
         s_obj = os.path.join(tmp, "sv_sol.o")
+        extra = [(os.path.join(tmp, name + ".o"), os.path.join(CSRC, name + ".hip"))
+                 for name in ("sv_tree_attn", "sv_tree_verify", "sv_cache")]
+        t_obj = os.path.join(tmp, "sv_tree_api.o")
         cmds = [
             [cc, "-x", "hip", "--offload-arch=" + ARCH, *COMMON_FLAGS, *DEVICE_FLAGS, "-c",
              os.path.join(CSRC, "sv_kernels.hip"), "-o", k_obj],
@@ -50,14 +54,22 @@ def build(verbose: bool = False) -> str:
             [cc, *COMMON_FLAGS, "-D__HIP_PLATFORM_AMD__", "-c", os.path.join(CSRC, "sv_api.cpp"), "-o", a_obj],
             [cc, *COMMON_FLAGS, "-c", os.path.join(CSRC, "sv_grid.cpp"), "-o", g_obj],
             [cc, *COMMON_FLAGS, "-D__HIP_PLATFORM_AMD__", "-c", os.path.join(CSRC, "sv_control.cpp"), "-o", c_obj],
+            [cc, *COMMON_FLAGS, "-D__HIP_PLATFORM_AMD__", "-c", os.path.join(CSRC, "sv_tree_api.cpp"), "-o", t_obj],
         ]
+        for obj, src in extra:
+            cmds.append([cc, "-x", "hip", "--offload-arch=" + ARCH, *COMMON_FLAGS, *DEVICE_FLAGS, "-c", src, "-o", obj])
         tmp_so = os.path.join(tmp, "libspecverify.so")
-        cmds.append([cc, "--offload-arch=" + ARCH, "-shared", "-fPIC", k_obj, l_obj, s_obj, a_obj, g_obj, c_obj,
-                     "-o", tmp_so])
-        for cmd in cmds:
+        link = [cc, "--offload-arch=" + ARCH, "-shared", "-fPIC", k_obj, l_obj, s_obj, a_obj, g_obj, c_obj, t_obj,
+                *[obj for obj, _ in extra], "-o", tmp_so]
+
+        def run(cmd):
             if verbose:
                 print(" ".join(cmd), flush=True)
             subprocess.check_call(cmd)
+
+        with ThreadPoolExecutor(4) as pool:  # one compiler process each
+            list(pool.map(run, cmds))
+        run(link)
         shutil.copyfile(tmp_so, LIB_PATH + ".tmp")
         os.replace(LIB_PATH + ".tmp", LIB_PATH)
     return LIB_PATH

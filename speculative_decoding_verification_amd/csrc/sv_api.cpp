@@ -408,7 +408,7 @@ const char* sv_status_str(sv_status status) {
         case SV_OK: return "SV_OK";
         case SV_ERR_NULL_ARG: return "SV_ERR_NULL_ARG: a required pointer is NULL";
         case SV_ERR_BAD_SHAPE: return "SV_ERR_BAD_SHAPE: batch < 0, k outside [1,64], vocab outside [1,2^24] or size overflow";
-        case SV_ERR_BAD_DTYPE: return "SV_ERR_BAD_DTYPE: dtype must be SV_F32 or SV_BF16";
+        case SV_ERR_BAD_DTYPE: return "SV_ERR_BAD_DTYPE: not a type that this call takes (logits: SV_F32, SV_BF16; cache: SV_BF16, SV_F16)";
         case SV_ERR_BAD_TEMPERATURE: return "SV_ERR_BAD_TEMPERATURE: temperature must be 0 or finite and >= 1e-4";
         case SV_ERR_WORKSPACE_TOO_SMALL: return "SV_ERR_WORKSPACE_TOO_SMALL: workspace_bytes below the size query";
         case SV_ERR_HIP: return "SV_ERR_HIP: a HIP launch, event record or stream query failed";
@@ -420,6 +420,8 @@ const char* sv_status_str(sv_status status) {
         case SV_ERR_CAPTURING: return "SV_ERR_CAPTURING: tagged calls cannot be captured into a HIP graph";
         case SV_ERR_SCRATCH_TOO_SMALL:
             return "SV_ERR_SCRATCH_TOO_SMALL: the call needs more than the built-in workspace (SV_NOALLOC_SCRATCH_BYTES)";
+        case SV_ERR_BAD_SCALE: return "SV_ERR_BAD_SCALE: the attention scale must be finite and > 0";
+        case SV_ERR_ALIASED: return "SV_ERR_ALIASED: two arrays that must be distinct are the same";
         default: return "unknown status";
     }
 }

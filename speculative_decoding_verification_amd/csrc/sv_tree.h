@@ -1,0 +1,140 @@
+// Internal interface between the C-ABI layer of the tree-drafting operators
+// (sv_tree_api.cpp) and their gfx950 kernels (sv_tree_attn.hip,
+// sv_tree_verify.hip, sv_cache.hip).  Not installed; not part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+namespace sv {
+
+// ---- attention of a tree over the paged cache --------------------------------
+
+// Workgroups of the attention kernel.  Each takes an equal share of the
+// batch's key tiles, so the count is also the number of partial-result slots
+// (two a workgroup) that the workspace holds.
+constexpr int kAttnWgs = 256;
+constexpr int kAttnStep = 32;  // keys one wavefront takes per step
+
+// Wavefronts per workgroup and row tiles of 16 query rows per workgroup: what
+// the staging buffers (160 KiB of LDS) and the accumulators (512 registers a
+// lane) hold.
+constexpr int attn_waves(int head_dim) { return head_dim > 128 ? 2 : 4; }
+constexpr int attn_max_row_tiles(int head_dim) { return head_dim > 128 ? 2 : 4; }
+
+struct AttnPlan {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* page_table;
+    const int32_t* seq_len;
+    const int32_t* parents;  // NULL when k == 0
+    void* out;
+    float* lse;              // may be NULL
+    float* part_acc;         // [slots][row_tiles * 16][head_dim]
+    float* part_ml;          // [slots][row_tiles * 16][2]
+    int64_t q_stride_b, q_stride_r, q_stride_h;
+    int32_t batch;
+    int32_t k;
+    int32_t q_heads, kv_heads, head_dim;
+    int32_t group;           // q_heads / kv_heads
+    int32_t rows;            // (k + 1) * group: query rows of one key head
+    int32_t row_tiles;       // 16-row tiles of one unit, 1 .. attn_max_row_tiles
+    int32_t row_units;       // units that share one key head's rows
+    int32_t n_pages, page_shift, max_pages;
+    int32_t is_f16;
+    float scale_log2;        // scale * log2(e)
+};
+
+hipError_t launch_tree_attention(const AttnPlan& p, hipStream_t stream);
+
+// ---- verification of a tree ---------------------------------------------------
+
+constexpr int kTreeThreads = 512;
+constexpr int kTreeMaxSlices = 64;
+
+enum TreeKind : int32_t { kTreeGreedy = 0, kTreeOneHot = 1, kTreeLogits = 2 };
+
+// One sequence's walk between two passes (workspace, 64-byte aligned).
+struct TreeState {
+    double m_t, z_t;     // target row of `at`: maximum of l / T (base 2), sum of 2^(l c2 - m)
+    double m_q, z_q;     // its draft row
+    double t, f;         // residual max(0, p - t q) and its mass F(t)
+    int32_t at;          // node whose children are tested, -1 the root
+    int32_t stage;       // what the next pass computes (TreeStage)
+    uint64_t left;       // children of `at` not yet tested
+    int32_t kept;        // nodes accepted so far
+    uint32_t arrived;    // workgroups that have handed in this pass's partial; 0 between passes
+    int32_t pad[6];
+};
+
+struct TreePlan {
+    const void* target;          // [B][k+1][V]
+    const void* draft;           // [B][draft_rows][V] or NULL
+    const int32_t* tokens;       // [B][k]
+    const int32_t* parents;      // [B][k]
+    const float* uniforms;       // [B][k+1] or NULL
+    int32_t* accepted_len;
+    int32_t* out_tokens;
+    int32_t* path;
+    TreeState* state;            // [B]
+    double* part;                // [B][kTreeMaxSlices][4]
+    int32_t batch, k, vocab, draft_rows;
+    int32_t kind;                // TreeKind
+    int32_t elem_bytes;          // 4 fp32, 2 bf16
+    int32_t vec;                 // rows start on 16-byte boundaries
+    double c2;                   // log2(e) / T
+};
+
+hipError_t launch_verify_tree(const TreePlan& p, hipStream_t stream);
+
+// ---- pages of the cache --------------------------------------------------------
+
+constexpr int kCacheMaxSeqs = 4096;  // what one workgroup's LDS holds in sv_cache_resize and sv_cache_fork
+
+struct CachePlan {
+    void* k_cache;
+    void* v_cache;
+    int32_t* page_table;     // [n_seqs][max_pages]
+    int32_t* page_count;     // [n_seqs]
+    int32_t* page_refs;      // [n_pages]
+    int32_t* seq_len;        // [n_seqs]
+    int32_t n_seqs, n_pages, page_shift, max_pages, n_layers, kv_heads, head_dim;
+};
+
+struct AppendPlan {
+    CachePlan c;             // page_count, page_refs unused; one layer
+    const void* k_new;
+    const void* v_new;
+    const int32_t* count;    // [n_seqs] or NULL
+    int64_t k_stride_b, k_stride_t, k_stride_h, v_stride_b, v_stride_t, v_stride_h;
+    int32_t t;
+};
+
+struct CommitPlan {
+    CachePlan c;
+    const int32_t* path;
+    const int32_t* accepted_len;
+    int32_t* new_len;
+    int32_t k;
+};
+
+struct ForkPlan {
+    CachePlan c;
+    const int32_t* src;
+    const int32_t* dst;
+    int32_t* status;
+    int32_t* claim;          // workspace: [n_seqs]
+    int32_t* new_page;       // workspace: [n]
+    int32_t* old_page;       // workspace: [n]
+    int32_t n;
+};
+
+hipError_t launch_cache_append(const AppendPlan& p, hipStream_t stream);
+hipError_t launch_cache_commit(const CommitPlan& p, hipStream_t stream);
+hipError_t launch_cache_fork(const ForkPlan& p, hipStream_t stream);
+hipError_t launch_cache_resize(const CachePlan& p, const int32_t* want_len, int32_t* status, hipStream_t stream);
+
+}  // namespace sv

@@ -1,0 +1,656 @@
+// gfx950 kernels of sv_tree_attention: the rows of a drafted tree (its root
+// and k nodes, several query heads to a key head) attend to a paged cache and
+// to their own ancestors.
+//
+// Mathematics.  Row r of key head h sees the committed keys, the root and its
+// ancestors: o_r = sum_j e^{s_rj - m_r} v_j / sum_j e^{s_rj - m_r}, s_rj =
+// scale q_r . k_j.  One pass over the keys with a running maximum m and sum l
+// (base 2: the scale carries log2 e); partial results (m, l, sum) over
+// disjoint key ranges join exactly as l = sum_i l_i 2^{m_i - m}.
+//
+//  k_tree_attn     Work is cut into key tiles of 32 keys per wavefront.  A unit
+//                  is one (sequence, key head, block of up to 64 query rows);
+//                  the tiles of all units stand in one line, and each of
+//                  kAttnWgs workgroups takes an equal run of it, whatever the
+//                  lengths of the sequences are: a single long sequence is
+//                  spread over the device and a ragged batch stays balanced,
+//                  with no host knowledge of the lengths.  Within a workgroup
+//                  the wavefronts take turns at 32-key steps, each with all of
+//                  the unit's rows, so a wavefront's keys and values pass
+//                  through LDS of its own and the loop holds no barrier.
+//                  K and V rows go from memory straight to LDS
+//                  (global_load_lds_dwordx4), two steps deep.  Scores are
+//                  formed transposed, S^T = K Q^T (v_mfma_f32_16x16x32), so a
+//                  lane holds keys of one query row: maxima and sums need two
+//                  lane exchanges, and the weights are in the operand layout of
+//                  O^T = V^T P^T as they stand.  V^T comes from row-major V by
+//                  the transposing LDS read (ds_read_b64_tr_b16).
+//                  The maximum is raised only when a score passes it by 2^8
+//                  (weights up to 256 are exact enough in 32-bit sums and in
+//                  the 16-bit operand, whose relative rounding is the same), so
+//                  most steps neither exchange lanes nor rescale.
+//                  Weights are rounded to the cache's 16-bit type for the
+//                  matrix product, relative 2^-9 (bf16) or 2^-12 (f16) each;
+//                  sums, maxima and products are 32-bit.
+//  k_tree_combine  Joins the partial results of units that several workgroups
+//                  share, in workgroup order (no atomics: reproducible), and
+//                  writes the zeros of absent sequences.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "specverify.h"
+#include "sv_tree.h"
+
+namespace sv {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef short shortx4_t __attribute__((ext_vector_type(4)));
+typedef short shortx8_t __attribute__((ext_vector_type(8)));
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
+
+constexpr float kRaise = 8.f;  // log2 by which a score may pass the running maximum
+constexpr int kXcdCount = 8;
+
+template <bool F16>
+__device__ __forceinline__ floatx4_t mma(shortx8_t a, shortx8_t b, floatx4_t c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b),
+                                                      c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ short to16(float x) {
+    if constexpr (F16)
+        return __builtin_bit_cast(short, static_cast<_Float16>(x));
+    else
+        return __builtin_bit_cast(short, static_cast<__bf16>(x));
+}
+
+template <bool F16>
+__device__ __forceinline__ float from16(uint16_t x) {
+    if constexpr (F16)
+        return static_cast<float>(__builtin_bit_cast(_Float16, x));
+    else
+        return __int_as_float(static_cast<int>(x) << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t x) {
+    constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+    return (x & e) == e;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 16-byte piece c of row r of a staged tile sits at piece c ^ swizzle(r), which
+// spreads the rows that one LDS read touches over the banks.  K reads take one
+// piece of 16 rows, V reads a pair of pieces of four rows; rows of 12 pieces
+// (head size 96) start at four different bank groups by themselves, and the
+// swizzle stays within groups of four pieces.
+template <int D>
+__device__ __forceinline__ int swizzle_k(int r) {
+    if constexpr (D == 96) return (r >> 2) & 3;
+    if constexpr (D == 64) return r & 7;
+    return r & 15;
+}
+template <int D>
+__device__ __forceinline__ int swizzle_v(int r) {
+    if constexpr (D == 96) return (r >> 1) & 2;
+    if constexpr (D == 64) return (2 * r) & 7;
+    return (2 * r) & 15;
+}
+
+// Ancestors of draft node `lane` as a bit mask (itself included; 0 for an
+// absent node: parent -2, out of range, or absent itself), by doubling.
+__device__ __forceinline__ uint64_t ancestors(const AttnPlan& p, int b, int lane) {
+    int up = -2;
+    if (lane < p.k) up = p.parents[static_cast<int64_t>(b) * p.k + lane];
+    if (up >= lane || up < -2) up = -2;
+    uint64_t mask = up == -2 ? 0 : (uint64_t{1} << lane);
+    bool gone = up == -2;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        const int from = up < 0 ? lane : up;
+        const uint64_t m = __shfl(static_cast<unsigned long long>(mask), from);
+        const int u = __shfl(up, from);
+        if (up >= 0) {
+            mask |= m;
+            up = u;
+        }
+        gone = gone || up == -2;
+    }
+    return gone ? 0 : mask;
+}
+
+// Key tiles of sequence b (0: absent, a negative length or one that its page
+// table row cannot hold).
+__device__ __forceinline__ int64_t seq_tiles(const AttnPlan& p, int b, int tile_keys) {
+    const int64_t n = p.seq_len[b];
+    const int64_t keys = n + p.k + 1;
+    if (n < 0 || keys > (static_cast<int64_t>(p.max_pages) << p.page_shift)) return 0;
+    return (keys + tile_keys - 1) / tile_keys;
+}
+
+// Inclusive sum over the workgroup's threads, and the total.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t* tmp) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(static_cast<long long>(v), d);
+        if (lane >= d) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) tmp[wave] = v;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        if (w < wave) v += tmp[w];
+        all += tmp[w];
+    }
+    *total = all;
+    return v;
+}
+
+// Tiles of one (key head, row block) of the whole batch.
+template <int NT>
+__device__ int64_t batch_tiles(const AttnPlan& p, int tile_keys, int64_t* tmp) {
+    int64_t sum = 0, all;
+    for (int b = threadIdx.x; b < p.batch; b += NT) sum += seq_tiles(p, b, tile_keys);
+    block_scan<NT>(sum, &all, tmp);
+    return all;
+}
+
+__host__ __device__ inline int64_t share_of(int64_t total) {
+    const int64_t w = (total + kAttnWgs - 1) / kAttnWgs;
+    return w > 0 ? w : 1;
+}
+
+template <bool F16, int D, int MT>
+__global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p) {
+    constexpr int NW = attn_waves(D);
+    constexpr int NT = NW * 64;
+    constexpr int STEP = kAttnStep;
+    constexpr int TILE = NW * STEP;           // keys of one tile: a step of each wavefront
+    constexpr int CH = D / 8;                 // 16-byte pieces of a row
+    constexpr int NL = STEP * CH / 64;        // direct-to-LDS loads of one step and operand
+    constexpr int KK = D / 32;                // matrix steps along the head
+    constexpr int DB = D / 16;                // output blocks along the head
+    static_assert(STEP * CH % 64 == 0 && 2 * NL < 63, "whole loads, countable");
+    // Two steps' K and V for each wavefront, each buffer its own array (so the
+    // compiler can tell a load into one from reads of another).  At the end of
+    // a run they hold the wavefronts' sums: one row tile takes 16 * D * 4 bytes
+    // a wavefront, which is one buffer.
+    __shared__ __attribute__((aligned(16))) uint16_t k0[NW * STEP * D];
+    __shared__ __attribute__((aligned(16))) uint16_t v0[NW * STEP * D];
+    __shared__ __attribute__((aligned(16))) uint16_t k1[NW * STEP * D];
+    __shared__ __attribute__((aligned(16))) uint16_t v1[NW * STEP * D];
+    __shared__ float wave_m[NW][MT * 16], wave_l[NW][MT * 16];
+    __shared__ uint64_t anc[SV_MAX_DRAFT];
+    __shared__ int64_t scan_tmp[NW];
+    __shared__ int64_t first_off;
+    __shared__ int first_b;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int q_of = lane & 15, g = lane >> 4;
+    // Blocks are dealt to the eight dies in turn: neighbours in the line of
+    // tiles (row blocks of one key head among them) run on one die.
+    const int wg = (blockIdx.x % kXcdCount) * (kAttnWgs / kXcdCount) + blockIdx.x / kXcdCount;
+    const int per_seq = p.kv_heads * p.row_units;
+    const int64_t total = batch_tiles<NT>(p, TILE, scan_tmp) * per_seq;
+    const int64_t share = share_of(total);
+    int64_t pos = wg * share;
+    const int64_t end = min(pos + share, total);
+    if (pos >= end) return;
+    {
+        int64_t base = 0;
+        for (int c = 0; base * per_seq <= pos; c += NT) {
+            const int b = c + tid;
+            const int64_t v = b < p.batch ? seq_tiles(p, b, TILE) : 0;
+            int64_t all;
+            const int64_t before = base + block_scan<NT>(v, &all, scan_tmp) - v;
+            if (v > 0 && pos >= before * per_seq && pos < (before + v) * per_seq) {
+                first_b = b;
+                first_off = before * per_seq;
+            }
+            base += all;
+        }
+        __syncthreads();
+    }
+    int b = first_b;
+    int64_t seq_off = first_off;  // the line's index of sequence b's first tile
+    int nt = static_cast<int>(seq_tiles(p, b, TILE));
+    bool new_seq = true;
+
+    const uint16_t* const kc = static_cast<const uint16_t*>(p.k_cache);
+    const uint16_t* const vc = static_cast<const uint16_t*>(p.v_cache);
+    const int page_mask = (1 << p.page_shift) - 1;
+
+    while (pos < end) {
+        while (pos >= seq_off + static_cast<int64_t>(nt) * per_seq) {  // the next sequence that has tiles
+            seq_off += static_cast<int64_t>(nt) * per_seq;
+            ++b;
+            nt = static_cast<int>(seq_tiles(p, b, TILE));
+            new_seq = true;
+        }
+        if (new_seq) {
+            __syncthreads();  // the previous sequence's readers of anc are done
+            if (wave == 0) {
+                const uint64_t m = ancestors(p, b, lane);
+                anc[lane] = m;
+            }
+            __syncthreads();
+            new_seq = false;
+        }
+        const int64_t in_seq = pos - seq_off;
+        const int unit = static_cast<int>(in_seq / nt);
+        const int t0 = static_cast<int>(in_seq - static_cast<int64_t>(unit) * nt);
+        const int t1 = static_cast<int>(min<int64_t>(nt, t0 + (end - pos)));
+        const int h = unit / p.row_units;
+        const int row0 = (unit - h * p.row_units) * (MT * 16);
+        const int len = p.seq_len[b];
+        const int keys = len + p.k + 1;
+        const uint64_t present = __ballot(anc[lane] != 0);
+        const int32_t* const table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+
+        shortx8_t qf[MT][KK];
+        uint64_t see[MT];  // the draft nodes that this lane's row sees
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = min(row0 + mt * 16 + q_of, p.rows - 1);
+            const int node = r / p.group, head = h * p.group + r - node * p.group;
+            see[mt] = node == 0 ? 0 : anc[node - 1];
+            const uint16_t* src = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(b) * p.q_stride_b +
+                                  static_cast<int64_t>(node) * p.q_stride_r + static_cast<int64_t>(head) * p.q_stride_h;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                qf[mt][kk] = *reinterpret_cast<const shortx8_t*>(src + (kk * 4 + g) * 8);
+        }
+        floatx4_t acc[MT][DB];
+        float m[MT], l[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            m[mt] = -__builtin_inff();
+            l[mt] = 0.f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) acc[mt][db] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        }
+
+        const int steps = t1 - t0;
+        const auto key_of = [&](int s) { return ((t0 + s) * NW + wave) * STEP; };
+        // The page of the position that lane (mod 32) stands for in step s, and
+        // the position's place in it.  Positions past the last key, and slots of
+        // absent nodes, may hold anything (a NaN would spoil a product even at
+        // weight 0): the root's row is read in their place.  Page numbers out of
+        // range are read as page 0: the result is then unspecified, the access
+        // in bounds.
+        const auto slot_of = [&](int s) {
+            const int key = key_of(s) + (lane & 31);
+            const int j = key - len - 1;
+            const bool there = j < 0 || (j < p.k && ((present >> j) & 1));
+            return there ? key : len;
+        };
+        const auto page_load = [&](int s) { return table[slot_of(min(s, steps - 1)) >> p.page_shift]; };
+        const auto dma = [&](uint16_t* ks, uint16_t* vs, int s, int page) {
+            const int place = slot_of(min(s, steps - 1)) & page_mask;
+            const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
+            const uint32_t row = ((id * p.kv_heads + h) << p.page_shift) + place;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int e = i * 64 + lane;
+                const int r = e / CH, c = e - r * CH;
+                const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(row), r))) * D;
+                __builtin_amdgcn_global_load_lds((const void*)(kc + at + ((c ^ swizzle_k<D>(r)) << 3)),
+                    (__attribute__((address_space(3))) void*)(ks + wave * (STEP * D) + i * 512), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds((const void*)(vc + at + ((c ^ swizzle_v<D>(r)) << 3)),
+                    (__attribute__((address_space(3))) void*)(vs + wave * (STEP * D) + i * 512), 16, 0, 0);
+            }
+        };
+        const auto compute = [&](uint16_t* ks_all, uint16_t* vs_all, int s) {
+            const int key0 = key_of(s);
+            if (key0 >= keys) return;
+            const uint16_t* const ks = ks_all + wave * (STEP * D);
+            uint16_t* const vs = vs_all + wave * (STEP * D);
+            floatx4_t sc[MT][2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int r = kb * 16 + q_of;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) sc[mt][kb] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    const shortx8_t a =
+                        *reinterpret_cast<const shortx8_t*>(ks + r * D + (((kk * 4 + g) ^ swizzle_k<D>(r)) << 3));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) sc[mt][kb] = mma<F16>(a, qf[mt][kk], sc[mt][kb]);
+                }
+            }
+            const bool tail = key0 + STEP > len;  // some keys are not committed ones
+            uint32_t seen[MT];                    // tail: which of the lane's 8 keys its row sees
+            if (tail) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    seen[mt] = 0;
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb) {
+                        // of the draft node at the lane's first key; -1 is the root, committed keys are below
+                        const int j = key0 + kb * 16 + g * 4 - len - 1;
+                        const uint32_t low = j >= 0 ? static_cast<uint32_t>(j < 64 ? see[mt] >> j : 0)
+                                                    : static_cast<uint32_t>(see[mt] << min(-j, 4)) | ((1u << min(-j, 4)) - 1);
+                        seen[mt] |= (low & 15u) << (kb * 4);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sc[mt][i >> 2][i & 3] = (seen[mt] >> i) & 1 ? sc[mt][i >> 2][i & 3] : -__builtin_inff();
+                }
+            }
+            bool raise = false;
+            float top[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float t = sc[mt][0][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) t = fmaxf(t, sc[mt][i >> 2][i & 3]);
+                top[mt] = t * p.scale_log2;
+                raise = raise || top[mt] > m[mt] + kRaise;
+            }
+            if (__any(raise)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float t = fmaxf(top[mt], __shfl_xor(top[mt], 16));
+                    t = fmaxf(t, __shfl_xor(t, 32));
+                    const float mn = fmaxf(m[mt], t);
+                    const float a = m[mt] == mn ? 1.f : exp2_fast(m[mt] - mn);
+                    m[mt] = mn;
+                    l[mt] *= a;
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) acc[mt][db] *= a;
+                }
+            }
+            shortx8_t pf[MT];
+            float w[MT][8];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float ms = m[mt] == -__builtin_inff() ? 0.f : m[mt];
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    w[mt][i] = exp2_fast(__builtin_fmaf(sc[mt][i >> 2][i & 3], p.scale_log2, -ms));
+                    sum += w[mt][i];
+                    pf[mt][i] = to16<F16>(w[mt][i]);
+                }
+                l[mt] += sum;
+            }
+            if (tail) {
+                // A value that is not finite must reach only the rows that see
+                // its node, and the matrix product would multiply it by the
+                // other rows' zero weights.  Such values (there are hardly ever
+                // any) are added one by one and cleared.
+                bool odd = false;
+                for (int e = lane; e < STEP * D; e += 64) odd = odd || nonfinite16<F16>(vs[e]);
+                if (__any(odd)) {
+                    for (int r = 0; r < STEP; ++r) {
+                        const int from = q_of + 16 * ((r & 15) >> 2), slot = (r >> 4) * 4 + (r & 3);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            float mine = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) mine = slot == i ? w[mt][i] : mine;
+                            const float wr = __shfl(mine, from);
+                            const bool sees = (__shfl(seen[mt], from) >> slot) & 1;
+#pragma unroll
+                            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int d = db * 16 + g * 4 + i;
+                                    const uint16_t x = vs[r * D + (((d >> 3) ^ swizzle_v<D>(r)) << 3) + (d & 7)];
+                                    if (sees && nonfinite16<F16>(x)) acc[mt][db][i] += wr * from16<F16>(x);
+                                }
+                        }
+                    }
+                    for (int e = lane; e < STEP * D; e += 64)
+                        if (nonfinite16<F16>(vs[e])) vs[e] = 0;
+                }
+            }
+            // Key slot j of the product's lane group g is key 4g + j of the
+            // first 16 keys, for j >= 4 key 4g + j - 4 of the second: the
+            // weights stand so already, and the transposing read gives each
+            // lane four keys of one column.
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                shortx8_t a;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const int r = kb * 16 + g * 4 + (q_of >> 2);
+                    const int c = db * 2 + ((q_of & 3) >> 1);
+                    const shortx4_t t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_shortx4_t*)(vs + r * D + ((c ^ swizzle_v<D>(r)) << 3) + (q_of & 1) * 4));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[kb * 4 + i] = t[i];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[mt][db] = mma<F16>(a, pf[mt], acc[mt][db]);
+            }
+        };
+        const auto step_wait = [&]() {
+            // All but the next step's loads have landed.
+            __builtin_amdgcn_s_waitcnt(0x0F70 | ((2 * NL) & 15) | (((2 * NL) >> 4) << 14));
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");
+        };
+        const auto reads_done = [&]() {
+            // Every LDS read of the step has returned: its buffers may be filled again.
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // Past the last step the loads repeat the last one's rows, so that the
+        // counts stay the same.  The page numbers of a step are asked for one
+        // step before its rows are, ahead of that step's loads.
+        int pa = page_load(0), pb = page_load(1), pc = page_load(2);
+        dma(k0, v0, 0, pa);
+        dma(k1, v1, 1, pb);
+        for (int s = 0; s < steps; s += 2) {
+            step_wait();
+            compute(k0, v0, s);
+            reads_done();
+            pa = page_load(s + 3);
+            dma(k0, v0, s + 2, pc);
+            __builtin_amdgcn_sched_barrier(0);
+            step_wait();
+            if (s + 1 < steps) compute(k1, v1, s + 1);
+            reads_done();
+            pc = page_load(s + 4);
+            dma(k1, v1, s + 3, pa);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // no load may land in a buffer that holds sums
+        asm volatile("" ::: "memory");
+
+        // Join the wavefronts.
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float t = l[mt] + __shfl_xor(l[mt], 16);
+            t += __shfl_xor(t, 32);
+            if (g == 0) {
+                wave_m[wave][mt * 16 + q_of] = m[mt];
+                wave_l[wave][mt * 16 + q_of] = t;
+            }
+        }
+        __syncthreads();  // and every wavefront has left the buffers
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float mm = wave_m[0][mt * 16 + q_of];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][mt * 16 + q_of]);
+            const float a = m[mt] == -__builtin_inff() ? 0.f : (m[mt] == mm ? 1.f : exp2_fast(m[mt] - mm));
+            float* const buf = reinterpret_cast<float*>(mt == 0 ? k0 : mt == 1 ? v0 : mt == 2 ? k1 : v1);
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                const int c = (db * 4 + g) ^ (q_of & 7);
+                *reinterpret_cast<floatx4_t*>(buf + (wave * 16 + q_of) * D + c * 4) = acc[mt][db] * a;
+            }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == nt;
+        // A workgroup's first slot takes a run that it begins with, its second
+        // one that goes on in the next workgroup.
+        const int64_t slot = static_cast<int64_t>(wg) * 2 + (pos == wg * share ? 0 : 1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const float* const buf = reinterpret_cast<const float*>(mt == 0 ? k0 : mt == 1 ? v0 : mt == 2 ? k1 : v1);
+            for (int e = tid; e < 16 * (D / 4); e += NT) {
+                const int r = e / (D / 4), c4 = e - r * (D / 4);
+                const int lr = mt * 16 + r;
+                floatx4_t o{0.f, 0.f, 0.f, 0.f};
+                float mm = wave_m[0][lr], ll = 0.f;
+#pragma unroll
+                for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][lr]);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    o += *reinterpret_cast<const floatx4_t*>(buf + (w * 16 + r) * D + ((c4 ^ (r & 7)) << 2));
+                    const float mw = wave_m[w][lr];
+                    ll += mw == -__builtin_inff() ? 0.f : wave_l[w][lr] * (mw == mm ? 1.f : exp2_fast(mw - mm));
+                }
+                if (whole) {
+                    const int row = row0 + lr;
+                    if (row < p.rows) {
+                        const int node = row / p.group, head = h * p.group + row - node * p.group;
+                        const bool there = node == 0 || anc[node - 1] != 0;
+                        const int64_t at = (static_cast<int64_t>(b) * (p.k + 1) + node) * p.q_heads + head;
+                        const float inv = 1.f / ll;
+                        shortx4_t x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = there ? to16<F16>(o[i] * inv) : short{0};
+                        *reinterpret_cast<shortx4_t*>(static_cast<uint16_t*>(p.out) + at * D + c4 * 4) = x;
+                        if (p.lse && c4 == 0)
+                            p.lse[at] = there ? (mm + __log2f(ll)) * 0.69314718055994531f : -__builtin_inff();
+                    }
+                } else {
+                    *reinterpret_cast<floatx4_t*>(p.part_acc + (slot * (MT * 16) + lr) * D + c4 * 4) = o;
+                    if (c4 == 0) {
+                        p.part_ml[(slot * (MT * 16) + lr) * 2] = mm;
+                        p.part_ml[(slot * (MT * 16) + lr) * 2 + 1] = ll;
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the buffers are free again
+        pos += steps;
+    }
+}
+
+// One workgroup of four wavefronts joins up to four rows of one unit.
+template <bool F16>
+__global__ __launch_bounds__(256) void k_tree_combine(AttnPlan p) {
+    __shared__ int64_t scan_tmp[4];
+    __shared__ uint64_t anc[SV_MAX_DRAFT];
+    const int tile_keys = attn_waves(p.head_dim) * kAttnStep;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per_seq = p.kv_heads * p.row_units;
+    const int b = blockIdx.x / per_seq;
+    const int unit = blockIdx.x - b * per_seq;
+    const int64_t total = batch_tiles<256>(p, tile_keys, scan_tmp) * per_seq;
+    const int64_t share = share_of(total);
+    int64_t before = 0;
+    for (int i = tid; i < b; i += 256) before += seq_tiles(p, i, tile_keys);
+    int64_t all;
+    block_scan<256>(before, &all, scan_tmp);
+    const int64_t nt = seq_tiles(p, b, tile_keys);
+    const int64_t off = all * per_seq + unit * nt;
+    const int64_t w0 = off / share, w1 = nt > 0 ? (off + nt - 1) / share : w0 - 1;
+    if (w0 == w1) return;  // one workgroup held all of it
+    if (wave == 0) {
+        const uint64_t m = ancestors(p, b, lane);
+        anc[lane] = m;
+    }
+    __syncthreads();
+    const int D = p.head_dim;
+    const int unit_rows = p.row_tiles * 16;
+    const int h = unit / p.row_units;
+    const int lr = blockIdx.y * 4 + wave;
+    const int row = (unit - h * p.row_units) * unit_rows + lr;
+    if (row >= p.rows) return;
+    const int node = row / p.group, head = h * p.group + row - node * p.group;
+    const int64_t at = (static_cast<int64_t>(b) * (p.k + 1) + node) * p.q_heads + head;
+    uint16_t* const out = static_cast<uint16_t*>(p.out) + at * D;
+    const bool there = nt > 0 && (node == 0 || anc[node - 1] != 0);
+    const int c = lane * 4;  // a lane takes four columns
+    if (!there) {
+        if (c < D) *reinterpret_cast<shortx4_t*>(out + c) = shortx4_t{0, 0, 0, 0};
+        if (p.lse && lane == 0) p.lse[at] = -__builtin_inff();
+        return;
+    }
+    const auto slot_row = [&](int64_t w) {
+        const int64_t slot = w * 2 + (w == w0 && off > w * share ? 1 : 0);
+        return slot * unit_rows + lr;
+    };
+    float mm = -__builtin_inff();
+    for (int64_t w = w0 + lane; w <= w1; w += 64) mm = fmaxf(mm, p.part_ml[slot_row(w) * 2]);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+    float ll = 0.f;
+    floatx4_t o{0.f, 0.f, 0.f, 0.f};
+    for (int64_t w = w0; w <= w1; ++w) {
+        const int64_t r = slot_row(w);
+        const float mw = p.part_ml[r * 2], lw = p.part_ml[r * 2 + 1];
+        const float a = mw == -__builtin_inff() ? 0.f : (mw == mm ? 1.f : exp2_fast(mw - mm));
+        ll += lw * a;
+        if (c < D) o += *reinterpret_cast<const floatx4_t*>(p.part_acc + r * D + c) * a;
+    }
+    const float inv = 1.f / ll;
+    if (c < D) {
+        shortx4_t x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = to16<F16>(o[i] * inv);
+        *reinterpret_cast<shortx4_t*>(out + c) = x;
+    }
+    if (p.lse && lane == 0) p.lse[at] = (mm + __log2f(ll)) * 0.69314718055994531f;
+}
+
+template <bool F16, int D>
+hipError_t launch_d(const AttnPlan& p, hipStream_t stream) {
+    const dim3 grid(kAttnWgs), block(attn_waves(D) * 64);
+    switch (p.row_tiles) {
+        case 1: k_tree_attn<F16, D, 1><<<grid, block, 0, stream>>>(p); break;
+        case 2: k_tree_attn<F16, D, 2><<<grid, block, 0, stream>>>(p); break;
+        case 3:
+            if constexpr (attn_max_row_tiles(D) >= 3) k_tree_attn<F16, D, 3><<<grid, block, 0, stream>>>(p);
+            break;
+        default:
+            if constexpr (attn_max_row_tiles(D) >= 4) k_tree_attn<F16, D, 4><<<grid, block, 0, stream>>>(p);
+            break;
+    }
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_t(const AttnPlan& p, hipStream_t stream) {
+    hipError_t e;
+    switch (p.head_dim) {
+        case 64: e = launch_d<F16, 64>(p, stream); break;
+        case 96: e = launch_d<F16, 96>(p, stream); break;
+        case 128: e = launch_d<F16, 128>(p, stream); break;
+        default: e = launch_d<F16, 256>(p, stream); break;
+    }
+    if (e != hipSuccess) return e;
+    const dim3 grid(static_cast<uint32_t>(p.batch) * p.kv_heads * p.row_units, p.row_tiles * 4);
+    k_tree_combine<F16><<<grid, dim3(256), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_tree_attention(const AttnPlan& p, hipStream_t stream) {
+    return p.is_f16 ? launch_t<true>(p, stream) : launch_t<false>(p, stream);
+}
+
+}  // namespace sv
