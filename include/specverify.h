@@ -601,7 +601,7 @@ sv_status sv_tree_attention(const sv_tree_attention_desc* desc, const void* q, c
 
 /* Shape and options of one sv_verify_tree call. */
 typedef struct sv_verify_tree_desc {
-    int32_t B;                 /* sequences, >= 0 */
+    int32_t B;                 /* sequences, in [0, 65535] */
     int32_t k;                 /* draft nodes per sequence, in [1, 64] */
     int32_t V;                 /* vocabulary size, in [1, 2^24] */
     int32_t draft_rows;        /* rows of draft_logits per sequence, in [1, k+1]; unused (any value) without them */

@@ -54,20 +54,24 @@ hipError_t launch_tree_attention(const AttnPlan& p, hipStream_t stream);
 
 constexpr int kTreeThreads = 512;
 constexpr int kTreeMaxSlices = 64;
+constexpr int kTreeMaxBatch = 65535;
+constexpr int kTreeWgs = 1024;   // workgroups of one pass, about
+constexpr int kTreePasses = 8;   // passes by several workgroups per sequence before one finishes the walk
+constexpr int kTreeTile = kTreeThreads * 8;  // tokens one workgroup takes at a time
+constexpr int64_t kTreeAllRows = int64_t{48} << 20;  // logits up to which every row is read at once
 
 enum TreeKind : int32_t { kTreeGreedy = 0, kTreeOneHot = 1, kTreeLogits = 2 };
 
 // One sequence's walk between two passes (workspace, 64-byte aligned).
 struct TreeState {
-    double m_t, z_t;     // target row of `at`: maximum of l / T (base 2), sum of 2^(l c2 - m)
+    double m_t, z_t;     // target row of `at`: whole power of two m >= max l c2, sum of 2^(l c2 - m)
     double m_q, z_q;     // its draft row
     double t, f;         // residual max(0, p - t q) and its mass F(t)
     int32_t at;          // node whose children are tested, -1 the root
     int32_t stage;       // what the next pass computes (TreeStage)
     uint64_t left;       // children of `at` not yet tested
     int32_t kept;        // nodes accepted so far
-    uint32_t arrived;    // workgroups that have handed in this pass's partial; 0 between passes
-    int32_t pad[6];
+    int32_t pad[7];
 };
 
 struct TreePlan {
@@ -79,8 +83,12 @@ struct TreePlan {
     int32_t* accepted_len;
     int32_t* out_tokens;
     int32_t* path;
-    TreeState* state;            // [B]
-    double* part;                // [B][kTreeMaxSlices][4]
+    uint32_t* arrived;           // [kTreeMaxBatch]: workgroups that have handed in a pass's partial; 0 between passes
+    TreeState* state;            // [B]: written by a call's first pass before its second reads it
+    double* part;                // [B][kTreeMaxSlices][4]: one pass's partials
+    double* row_part;            // [B][k+1+draft_rows][kTreeMaxSlices][2]: every row's, or NULL (rows read as the walk comes to them)
+    int64_t per, row_per;        // tokens of one slice: of a pass, and where every row is read at once
+    int32_t slices, row_slices;  // workgroups on one row
     int32_t batch, k, vocab, draft_rows;
     int32_t kind;                // TreeKind
     int32_t elem_bytes;          // 4 fp32, 2 bf16

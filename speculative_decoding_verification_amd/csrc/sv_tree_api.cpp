@@ -71,9 +71,18 @@ size_t attention_bytes(const AttnPlan& p) {
            align_up(attention_slot_rows(p) * 2 * sizeof(float));
 }
 
+// As many slices of whole tiles to a row as make about kTreeWgs workgroups on `rows` rows.
+void tree_slices(int64_t vocab, int64_t rows, int64_t* per, int32_t* slices) {
+    const int64_t tiles = (vocab + kTreeTile - 1) / kTreeTile;
+    int64_t n = (tiles + kTreeMaxSlices - 1) / kTreeMaxSlices;
+    while (n < tiles && (tiles + n - 1) / n * rows > kTreeWgs) ++n;
+    *per = n * kTreeTile;
+    *slices = static_cast<int32_t>((tiles + n - 1) / n);
+}
+
 sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     if (!d) return SV_ERR_NULL_ARG;
-    if (d->B < 0 || d->k < 1 || d->k > SV_MAX_DRAFT || d->V < 1 || d->V > (1 << 24)) return SV_ERR_BAD_SHAPE;
+    if (d->B < 0 || d->B > kTreeMaxBatch || d->k < 1 || d->k > SV_MAX_DRAFT || d->V < 1 || d->V > (1 << 24)) return SV_ERR_BAD_SHAPE;
     if (d->dtype != SV_F32 && d->dtype != SV_BF16) return SV_ERR_BAD_DTYPE;
     if (d->draft_kind != SV_DRAFT_LOGITS && d->draft_kind != SV_DRAFT_ONEHOT) return SV_ERR_BAD_DRAFT_KIND;
     const float t = d->temperature;
@@ -86,15 +95,30 @@ sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     p->draft_rows = p->kind == kTreeLogits ? d->draft_rows : 0;
     p->elem_bytes = d->dtype == SV_BF16 ? 2 : 4;
     p->c2 = t == 0.f ? 0.0 : kLog2E / static_cast<double>(t);
+    tree_slices(p->vocab, p->batch, &p->per, &p->slices);
+    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows), &p->row_per, &p->row_slices);
     return SV_OK;
 }
 
 size_t tree_state_bytes(int64_t batch) { return align_up(static_cast<size_t>(batch) * sizeof(TreeState)); }
 
+// The arrival counts are what one call leaves to the next (all 0), so they
+// stand at the same place whatever the shape: words of another call's shape
+// never lie where counts are.
+constexpr size_t kTreeCountBytes = (static_cast<size_t>(kTreeMaxBatch) * sizeof(uint32_t) + kAlign - 1) & ~(kAlign - 1);
+
+size_t tree_part_bytes(int64_t batch) { return align_up(static_cast<size_t>(batch) * kTreeMaxSlices * 4 * sizeof(double)); }
+
+// Whether the statistics of every row are taken at once.
+bool all_rows(const TreePlan& p) {
+    return p.slices > 1 && static_cast<int64_t>(p.batch) * (p.k + 1 + p.draft_rows) * p.vocab <= kTreeAllRows;
+}
+
 size_t tree_bytes(const TreePlan& p) {
-    const size_t n = tree_state_bytes(p.batch) +
-                     align_up(static_cast<size_t>(p.batch) * kTreeMaxSlices * 4 * sizeof(double));
-    return n < kAlign ? kAlign : n;
+    size_t n = kTreeCountBytes + tree_state_bytes(p.batch) + tree_part_bytes(p.batch);
+    if (all_rows(p))
+        n += align_up(static_cast<size_t>(p.batch) * (p.k + 1 + p.draft_rows) * kTreeMaxSlices * 2 * sizeof(double));
+    return n;
 }
 
 sv_status plan_cache(const sv_cache_desc* d, CachePlan* p) {
@@ -195,8 +219,12 @@ sv_status sv_verify_tree(const sv_verify_tree_desc* desc, const void* target_log
     p.accepted_len = accepted_len;
     p.out_tokens = out_tokens;
     p.path = path_out;
-    p.state = static_cast<sv::TreeState*>(workspace);
-    p.part = reinterpret_cast<double*>(static_cast<char*>(workspace) + sv::tree_state_bytes(p.batch));
+    p.arrived = static_cast<uint32_t*>(workspace);
+    char* base = static_cast<char*>(workspace) + sv::kTreeCountBytes;
+    p.state = reinterpret_cast<sv::TreeState*>(base);
+    base += sv::tree_state_bytes(p.batch);
+    p.part = reinterpret_cast<double*>(base);
+    p.row_part = sv::all_rows(p) ? reinterpret_cast<double*>(base + sv::tree_part_bytes(p.batch)) : nullptr;
     p.vec = static_cast<int64_t>(p.vocab) * p.elem_bytes % 16 == 0 && sv::aligned(target_logits, 16) &&
             (!p.draft || sv::aligned(p.draft, 16));
     return sv::launched(sv::launch_verify_tree(p, stream));

@@ -425,6 +425,22 @@ def test_walk_repeats_on_one_workspace_and_in_a_graph(dev):
         sv.verify_tree(t, d, tok, par, u, 1.0)
 
 
+def test_walk_calls_of_other_shapes_on_one_workspace(dev):
+    """A workspace serves calls of any shape in turn: small and large batches, every row at once and rows read as the walk
+    comes to them, one and several workgroups per row."""
+    on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=dev)
+    shapes = [(1, 20, 9000, False), (60, 6, 5000, False), (3, 4, 40, True), (2, 30, 30000, True), (90, 3, 9000, False),
+              (1, 2, 100000, False), (300, 2, 4500, True)]
+    for i, (B, k, V, onehot) in enumerate(shapes + shapes):
+        t, d, tok, par, u = logits_case(i, B, k, V, 1.0, onehot)
+        args = (on(t), None if onehot else on(d), on(tok), on(par), on(u), 1.0)
+        want = sv.verify_tree(*args, onehot=onehot, workspace=torch.zeros(1 << 24, dtype=torch.uint8, device=dev))
+        got = sv.verify_tree(*args, onehot=onehot, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (B, k, V, onehot)
+        assert int(got.accepted_len.min()) >= 0
+
+
 # ------------------------------------------------------------------------------------------------------- the cache
 
 def same_bits(a, b):
