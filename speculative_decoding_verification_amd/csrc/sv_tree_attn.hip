@@ -38,6 +38,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "specverify.h"
 #include "sv_tree.h"
@@ -106,6 +107,76 @@ __device__ __forceinline__ int swizzle_v(int r) {
     if constexpr (D == 64) return (2 * r) & 7;
     return (2 * r) & 15;
 }
+
+// The staged operands are read in inline assembly that waits for what it
+// reads: the compiler cannot tell a transposing read from the loads in flight
+// to the other buffers and would wait for all of them.  A K read takes the
+// lane's pieces kk of its row, a V read four keys of one column in each half
+// of the step.  `half` is the byte offset of the step's second 16 rows.
+template <int D>
+struct KReader {  // byte address of piece kk: for powers of two the swizzle is an exclusive or of the address
+    uint32_t base;
+    __device__ __forceinline__ KReader(uint32_t lds, int row, int g) {
+        base = lds + row * (D * 2) + ((g ^ swizzle_k<D>(row)) << 4);
+    }
+    __device__ __forceinline__ uint32_t at(int kk) const { return D == 96 ? base + kk * 64 : base ^ (kk << 6); }
+    template <int HALF>
+    __device__ __forceinline__ void read(shortx8_t (&a)[D / 32]) const {
+        constexpr int off = HALF * 16 * D * 2;
+        if constexpr (D == 64)
+            asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(a[1]) : "v"(at(0)), "v"(at(1)), "n"(off) : "memory");
+        else if constexpr (D == 96)
+            asm volatile("ds_read_b128 %0, %3 offset:%4\n\tds_read_b128 %1, %3 offset:%5\n\t"
+                         "ds_read_b128 %2, %3 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2])
+                         : "v"(base), "n"(off), "n"(off + 64), "n"(off + 128) : "memory");
+        else
+#pragma unroll
+            for (int i = 0; i < D / 32; i += 4)
+                asm volatile("ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+                             "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(a[i]), "=&v"(a[i + 1]), "=&v"(a[i + 2]), "=&v"(a[i + 3])
+                             : "v"(at(i)), "v"(at(i + 1)), "v"(at(i + 2)), "v"(at(i + 3)), "n"(off) : "memory");
+    }
+};
+
+template <int D>
+struct VReader {
+    static constexpr int N = D == 96 ? 3 : 4;  // column blocks of 16 that one read takes
+    uint32_t base;
+    int odd;  // head size 96: what the swizzle adds to even blocks and takes from odd ones
+    __device__ __forceinline__ VReader(uint32_t lds, int lane) {
+        const int i = lane & 15, r = (lane >> 4) * 4 + (i >> 2), pair = (i & 3) >> 1, sw = swizzle_v<D>(r);
+        if constexpr (D == 96) {
+            odd = (sw >> 1) * 32;
+            base = lds + r * (D * 2) + pair * 16 + (i & 1) * 8;
+        } else {
+            odd = 0;
+            base = lds + r * (D * 2) + ((pair ^ sw) << 4) + (i & 1) * 8;
+        }
+    }
+    __device__ __forceinline__ uint32_t at(int db) const {
+        return D == 96 ? base + db * 32 + (db & 1 ? -odd : odd) : base ^ (db << 5);
+    }
+    __device__ __forceinline__ void read(int db, shortx4_t (&lo)[N], shortx4_t (&hi)[N]) const {
+        constexpr int half = 16 * D * 2;
+        if constexpr (N == 3)
+            asm volatile("ds_read_b64_tr_b16 %0, %6\n\tds_read_b64_tr_b16 %1, %6 offset:%9\n\t"
+                         "ds_read_b64_tr_b16 %2, %7\n\tds_read_b64_tr_b16 %3, %7 offset:%9\n\t"
+                         "ds_read_b64_tr_b16 %4, %8\n\tds_read_b64_tr_b16 %5, %8 offset:%9\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2])
+                         : "v"(at(db)), "v"(at(db + 1)), "v"(at(db + 2)), "n"(half) : "memory");
+        else
+            asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %4, %10\n\tds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %6, %11\n\tds_read_b64_tr_b16 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]),
+                           "=&v"(lo[3]), "=&v"(hi[3])
+                         : "v"(at(db)), "v"(at(db + 1)), "v"(at(db + 2)), "v"(at(db + 3)), "n"(half) : "memory");
+    }
+};
 
 // Ancestors of draft node `lane` as a bit mask (itself included; 0 for an
 // absent node: parent -2, out of range, or absent itself), by doubling.
@@ -185,19 +256,17 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     constexpr int KK = D / 32;                // matrix steps along the head
     constexpr int DB = D / 16;                // output blocks along the head
     static_assert(STEP * CH % 64 == 0 && 2 * NL < 63, "whole loads, countable");
-    // Two steps' K and V for each wavefront, each buffer its own array (so the
-    // compiler can tell a load into one from reads of another).  At the end of
-    // a run they hold the wavefronts' sums: one row tile takes 16 * D * 4 bytes
-    // a wavefront, which is one buffer.
-    __shared__ __attribute__((aligned(16))) uint16_t k0[NW * STEP * D];
-    __shared__ __attribute__((aligned(16))) uint16_t v0[NW * STEP * D];
-    __shared__ __attribute__((aligned(16))) uint16_t k1[NW * STEP * D];
-    __shared__ __attribute__((aligned(16))) uint16_t v1[NW * STEP * D];
+    // Two steps' K and V for each wavefront: [wavefront][K, V][step parity].
+    // At the end of a run they hold the wavefronts' sums, a buffer's size for
+    // each row tile.
+    constexpr int BUF = STEP * D;  // elements of one buffer
+    __shared__ __attribute__((aligned(1024))) uint16_t stage[NW * 4 * BUF];
     __shared__ float wave_m[NW][MT * 16], wave_l[NW][MT * 16];
     __shared__ uint64_t anc[SV_MAX_DRAFT];
     __shared__ int64_t scan_tmp[NW];
     __shared__ int64_t first_off;
     __shared__ int first_b;
+    __shared__ int wave_odd[NW];  // whether the wavefront met a tree row's value that is not finite
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int q_of = lane & 15, g = lane >> 4;
@@ -286,72 +355,97 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
 
         const int steps = t1 - t0;
         const auto key_of = [&](int s) { return ((t0 + s) * NW + wave) * STEP; };
-        // The page of the position that lane (mod 32) stands for in step s, and
-        // the position's place in it.  Positions past the last key, and slots of
-        // absent nodes, may hold anything (a NaN would spoil a product even at
-        // weight 0): the root's row is read in their place.  Page numbers out of
-        // range are read as page 0: the result is then unspecified, the access
-        // in bounds.
+        // Steps whose keys are all committed ones come first.
+        const int full = min(steps, max(0, (len - wave * STEP) / STEP + NW - 1) / NW - t0);
+        uint16_t* const mine = stage + wave * (4 * BUF);
+        const uint32_t lds = static_cast<uint32_t>(
+            reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t*)mine));
+        const KReader<D> kread(lds, q_of, g);
+        const VReader<D> vread(lds + 2 * BUF * 2, lane);
+        // Row of the cache (of head_dim elements) for the position that lane
+        // (mod 32) stands for in step s.  Positions past the last key, and slots
+        // of absent nodes, may hold anything (a NaN would spoil a product even
+        // at weight 0): the root's row is read in their place.  Page numbers out
+        // of range are read as page 0: the result is then unspecified, the
+        // access in bounds.
         const auto slot_of = [&](int s) {
-            const int key = key_of(s) + (lane & 31);
+            const int key = key_of(min(s, steps - 1)) + (lane & 31);
             const int j = key - len - 1;
-            const bool there = j < 0 || (j < p.k && ((present >> j) & 1));
-            return there ? key : len;
+            if (j < 0) return key;
+            return j < p.k && ((present >> j) & 1) ? key : len;
         };
-        const auto page_load = [&](int s) { return table[slot_of(min(s, steps - 1)) >> p.page_shift]; };
-        const auto dma = [&](uint16_t* ks, uint16_t* vs, int s, int page) {
-            const int place = slot_of(min(s, steps - 1)) & page_mask;
+        const auto page_load = [&](int s) { return table[slot_of(s) >> p.page_shift]; };
+        const auto row_of = [&](int s, int page) {
             const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
-            const uint32_t row = ((id * p.kv_heads + h) << p.page_shift) + place;
+            return ((id * p.kv_heads + h) << p.page_shift) + (slot_of(s) & page_mask);
+        };
+        // One operand's rows of a step, straight to LDS.  A load takes whole
+        // rows for the head sizes that are powers of two, and where these stand
+        // together in one page its address is one base for all lanes; otherwise
+        // every lane takes its row's.
+        const auto dma = [&](const uint16_t* cache, uint16_t* to, int s, uint32_t row, const auto& swizzle) {
+            constexpr int RPI = 512 / D;  // rows of one load
+            if (D != 96 && s < full && (1 << p.page_shift) >= RPI) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int e = i * 64 + lane;
-                const int r = e / CH, c = e - r * CH;
-                const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(row), r))) * D;
-                __builtin_amdgcn_global_load_lds((const void*)(kc + at + ((c ^ swizzle_k<D>(r)) << 3)),
-                    (__attribute__((address_space(3))) void*)(ks + wave * (STEP * D) + i * 512), 16, 0, 0);
-                __builtin_amdgcn_global_load_lds((const void*)(vc + at + ((c ^ swizzle_v<D>(r)) << 3)),
-                    (__attribute__((address_space(3))) void*)(vs + wave * (STEP * D) + i * 512), 16, 0, 0);
+                for (int i = 0; i < NL; ++i) {
+                    const int r = i * RPI + lane / CH, c = lane % CH;
+                    const uint32_t first = __builtin_amdgcn_readlane(row, i * RPI);
+                    const char* const base = reinterpret_cast<const char*>(cache) + static_cast<uint64_t>(first) * (D * 2);
+                    const uint32_t off = (lane / CH) * (D * 2) + ((c ^ swizzle(r)) << 4);
+                    __builtin_amdgcn_global_load_lds((const void*)(base + off),
+                        (__attribute__((address_space(3))) void*)(to + i * 512), 16, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const int e = i * 64 + lane;
+                    const int r = e / CH, c = e - r * CH;
+                    const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(row), r))) * D;
+                    __builtin_amdgcn_global_load_lds((const void*)(cache + at + ((c ^ swizzle(r)) << 3)),
+                        (__attribute__((address_space(3))) void*)(to + i * 512), 16, 0, 0);
+                }
             }
         };
-        const auto compute = [&](uint16_t* ks_all, uint16_t* vs_all, int s) {
-            const int key0 = key_of(s);
-            if (key0 >= keys) return;
-            const uint16_t* const ks = ks_all + wave * (STEP * D);
-            uint16_t* const vs = vs_all + wave * (STEP * D);
-            floatx4_t sc[MT][2];
+        const auto k_dma = [&](int s, uint32_t row) { dma(kc, mine + (s & 1) * BUF, s, row, swizzle_k<D>); };
+        const auto v_dma = [&](int s, uint32_t row) { dma(vc, mine + (2 + (s & 1)) * BUF, s, row, swizzle_v<D>); };
+        // Scores of step s, transposed: lane's row q_of, keys 16 kb + 4 g + i.
+        const auto scores = [&](int s, floatx4_t (&sc)[MT][2]) {
+            KReader<D> k = kread;
+            k.base += (s & 1) * (BUF * 2);
+            shortx8_t a[KK];
+            k.template read<0>(a);
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const int r = kb * 16 + q_of;
+            for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) sc[mt][kb] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+                for (int mt = 0; mt < MT; ++mt)
+                    sc[mt][0] = mma<F16>(a[kk], qf[mt][kk], kk ? sc[mt][0] : floatx4_t{0.f, 0.f, 0.f, 0.f});
+            k.template read<1>(a);
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const shortx8_t a =
-                        *reinterpret_cast<const shortx8_t*>(ks + r * D + (((kk * 4 + g) ^ swizzle_k<D>(r)) << 3));
+            for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) sc[mt][kb] = mma<F16>(a, qf[mt][kk], sc[mt][kb]);
+                for (int mt = 0; mt < MT; ++mt)
+                    sc[mt][1] = mma<F16>(a[kk], qf[mt][kk], kk ? sc[mt][1] : floatx4_t{0.f, 0.f, 0.f, 0.f});
+        };
+        // The scores that a row's ancestry hides become -inf.
+        const auto hide = [&](int s, floatx4_t (&sc)[MT][2]) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                uint32_t seen = 0;  // which of the lane's 8 keys its row sees
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    // of the draft node at the lane's first key; -1 is the root, committed keys are below
+                    const int j = key_of(s) + kb * 16 + g * 4 - len - 1;
+                    const uint32_t low = j >= 0 ? static_cast<uint32_t>(j < 64 ? see[mt] >> j : 0)
+                                                : static_cast<uint32_t>(see[mt] << min(-j, 4)) | ((1u << min(-j, 4)) - 1);
+                    seen |= (low & 15u) << (kb * 4);
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sc[mt][i >> 2][i & 3] = (seen >> i) & 1 ? sc[mt][i >> 2][i & 3] : -__builtin_inff();
             }
-            const bool tail = key0 + STEP > len;  // some keys are not committed ones
-            uint32_t seen[MT];                    // tail: which of the lane's 8 keys its row sees
-            if (tail) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    seen[mt] = 0;
-#pragma unroll
-                    for (int kb = 0; kb < 2; ++kb) {
-                        // of the draft node at the lane's first key; -1 is the root, committed keys are below
-                        const int j = key0 + kb * 16 + g * 4 - len - 1;
-                        const uint32_t low = j >= 0 ? static_cast<uint32_t>(j < 64 ? see[mt] >> j : 0)
-                                                    : static_cast<uint32_t>(see[mt] << min(-j, 4)) | ((1u << min(-j, 4)) - 1);
-                        seen[mt] |= (low & 15u) << (kb * 4);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sc[mt][i >> 2][i & 3] = (seen[mt] >> i) & 1 ? sc[mt][i >> 2][i & 3] : -__builtin_inff();
-                }
-            }
+        };
+        // Raises the maxima where a score passes them by 2^kRaise.
+        const auto raise_to = [&](const floatx4_t (&sc)[MT][2]) {
             bool raise = false;
             float top[MT];
 #pragma unroll
@@ -375,107 +469,114 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                     for (int db = 0; db < DB; ++db) acc[mt][db] *= a;
                 }
             }
-            shortx8_t pf[MT];
-            float w[MT][8];
+        };
+        const auto weights = [&](const floatx4_t (&sc)[MT][2], shortx8_t (&pf)[MT]) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const float ms = m[mt] == -__builtin_inff() ? 0.f : m[mt];
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    w[mt][i] = exp2_fast(__builtin_fmaf(sc[mt][i >> 2][i & 3], p.scale_log2, -ms));
-                    sum += w[mt][i];
-                    pf[mt][i] = to16<F16>(w[mt][i]);
+                    const float w = exp2_fast(__builtin_fmaf(sc[mt][i >> 2][i & 3], p.scale_log2, -ms));
+                    sum += w;
+                    pf[mt][i] = to16<F16>(w);
                 }
                 l[mt] += sum;
             }
+        };
+        // Key slot j of the product's lane group g is key 4g + j of the first
+        // 16 keys, for j >= 4 key 4g + j - 4 of the second: the weights stand so
+        // already, and the transposing read gives each lane four keys of one
+        // column.
+        const auto values = [&](int s, const shortx8_t (&pf)[MT]) {
+            VReader<D> v = vread;
+            v.base += (s & 1) * (BUF * 2);
+            constexpr int N = VReader<D>::N;
+#pragma unroll
+            for (int db = 0; db < DB; db += N) {
+                shortx4_t lo[N], hi[N];
+                v.read(db, lo, hi);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const shortx8_t a = __builtin_shufflevector(lo[n], hi[n], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) acc[mt][db + n] = mma<F16>(a, pf[mt], acc[mt][db + n]);
+                }
+            }
+        };
+        // A value that is not finite must reach only the rows that see its
+        // node, and the matrix product would multiply it by the other rows'
+        // zero weights.  Such values (there are hardly ever any) are cleared
+        // here and added where the sums are written.
+        bool odd = false;
+        const auto clear_odd = [&](int s) {
+            uint16_t* const vs = mine + (2 + (s & 1)) * BUF;
+#pragma unroll 1
+            for (int e = lane; e < BUF; e += 64)
+                if (nonfinite16<F16>(vs[e])) {
+                    vs[e] = 0;
+                    odd = true;
+                }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        };
+
+        // While step s is worked on, the scores of step s + 1 are formed (its K
+        // has landed), K of step s + 2 and V of steps s + 1 and s + 2 are on
+        // their way.  Page numbers are asked for one step ahead of the rows.
+        // Past the last step the loads repeat its rows, so that the count of
+        // loads in flight is the same at every wait.
+        constexpr int kOne = NL, kTwo = 2 * NL;
+        const auto landed = [&](auto left) {  // all but the last `left` loads
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0F70 | (decltype(left)::value & 15) | ((decltype(left)::value >> 4) << 14));
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        floatx4_t sc[MT][2], next[MT][2];
+        uint32_t row;
+        {
+            const int pa = page_load(0), pb = page_load(1), pc = page_load(2);
+            row = row_of(0, pa);
+            k_dma(0, row);
+            v_dma(0, row);
+            row = row_of(1, pb);
+            k_dma(1, row);
+            landed(std::integral_constant<int, kTwo>{});
+            scores(0, sc);
+            v_dma(1, row);
+            row = row_of(2, pc);
+        }
+        for (int s = 0; s < steps; ++s) {
+            landed(std::integral_constant<int, kOne>{});
+            const bool tail = s >= full;
+            if (tail && key_of(s) >= keys) break;  // nothing of this wavefront's is left
             if (tail) {
-                // A value that is not finite must reach only the rows that see
-                // its node, and the matrix product would multiply it by the
-                // other rows' zero weights.  Such values (there are hardly ever
-                // any) are added one by one and cleared.
-                bool odd = false;
-                for (int e = lane; e < STEP * D; e += 64) odd = odd || nonfinite16<F16>(vs[e]);
-                if (__any(odd)) {
-                    for (int r = 0; r < STEP; ++r) {
-                        const int from = q_of + 16 * ((r & 15) >> 2), slot = (r >> 4) * 4 + (r & 3);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            float mine = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) mine = slot == i ? w[mt][i] : mine;
-                            const float wr = __shfl(mine, from);
-                            const bool sees = (__shfl(seen[mt], from) >> slot) & 1;
-#pragma unroll
-                            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int d = db * 16 + g * 4 + i;
-                                    const uint16_t x = vs[r * D + (((d >> 3) ^ swizzle_v<D>(r)) << 3) + (d & 7)];
-                                    if (sees && nonfinite16<F16>(x)) acc[mt][db][i] += wr * from16<F16>(x);
-                                }
-                        }
-                    }
-                    for (int e = lane; e < STEP * D; e += 64)
-                        if (nonfinite16<F16>(vs[e])) vs[e] = 0;
-                }
+                hide(s, sc);
+                clear_odd(s);
             }
-            // Key slot j of the product's lane group g is key 4g + j of the
-            // first 16 keys, for j >= 4 key 4g + j - 4 of the second: the
-            // weights stand so already, and the transposing read gives each
-            // lane four keys of one column.
+            raise_to(sc);
+            const int page = page_load(s + 3);
+            k_dma(s + 2, row);
+            __builtin_amdgcn_sched_barrier(0);
+            shortx8_t pf[MT];
+            scores(s + 1, next);
+            weights(sc, pf);
+            values(s, pf);
+            __builtin_amdgcn_sched_barrier(0);
+            v_dma(s + 2, row);
+            row = row_of(s + 3, page);
 #pragma unroll
-            for (int db = 0; db < DB; ++db) {
-                shortx8_t a;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const int r = kb * 16 + g * 4 + (q_of >> 2);
-                    const int c = db * 2 + ((q_of & 3) >> 1);
-                    const shortx4_t t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (lds_shortx4_t*)(vs + r * D + ((c ^ swizzle_v<D>(r)) << 3) + (q_of & 1) * 4));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) a[kb * 4 + i] = t[i];
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) acc[mt][db] = mma<F16>(a, pf[mt], acc[mt][db]);
+            for (int mt = 0; mt < MT; ++mt) {
+                sc[mt][0] = next[mt][0];
+                sc[mt][1] = next[mt][1];
             }
-        };
-        const auto step_wait = [&]() {
-            // All but the next step's loads have landed.
-            __builtin_amdgcn_s_waitcnt(0x0F70 | ((2 * NL) & 15) | (((2 * NL) >> 4) << 14));
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("" ::: "memory");
-        };
-        const auto reads_done = [&]() {
-            // Every LDS read of the step has returned: its buffers may be filled again.
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0xC07F);
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        // Past the last step the loads repeat the last one's rows, so that the
-        // counts stay the same.  The page numbers of a step are asked for one
-        // step before its rows are, ahead of that step's loads.
-        int pa = page_load(0), pb = page_load(1), pc = page_load(2);
-        dma(k0, v0, 0, pa);
-        dma(k1, v1, 1, pb);
-        for (int s = 0; s < steps; s += 2) {
-            step_wait();
-            compute(k0, v0, s);
-            reads_done();
-            pa = page_load(s + 3);
-            dma(k0, v0, s + 2, pc);
-            __builtin_amdgcn_sched_barrier(0);
-            step_wait();
-            if (s + 1 < steps) compute(k1, v1, s + 1);
-            reads_done();
-            pc = page_load(s + 4);
-            dma(k1, v1, s + 3, pa);
-            __builtin_amdgcn_sched_barrier(0);
         }
         __builtin_amdgcn_s_waitcnt(0x0F70);  // no load may land in a buffer that holds sums
         asm volatile("" ::: "memory");
 
         // Join the wavefronts.
+        odd = __any(odd);
+        if (lane == 0) wave_odd[wave] = odd;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float t = l[mt] + __shfl_xor(l[mt], 16);
@@ -492,7 +593,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
 #pragma unroll
             for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][mt * 16 + q_of]);
             const float a = m[mt] == -__builtin_inff() ? 0.f : (m[mt] == mm ? 1.f : exp2_fast(m[mt] - mm));
-            float* const buf = reinterpret_cast<float*>(mt == 0 ? k0 : mt == 1 ? v0 : mt == 2 ? k1 : v1);
+            float* const buf = reinterpret_cast<float*>(stage) + mt * (NW * 16 * D);
 #pragma unroll
             for (int db = 0; db < DB; ++db) {
                 const int c = (db * 4 + g) ^ (q_of & 7);
@@ -501,12 +602,15 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == nt;
+        int any_odd = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) any_odd |= wave_odd[w];
         // A workgroup's first slot takes a run that it begins with, its second
         // one that goes on in the next workgroup.
         const int64_t slot = static_cast<int64_t>(wg) * 2 + (pos == wg * share ? 0 : 1);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const float* const buf = reinterpret_cast<const float*>(mt == 0 ? k0 : mt == 1 ? v0 : mt == 2 ? k1 : v1);
+            const float* const buf = reinterpret_cast<const float*>(stage) + mt * (NW * 16 * D);
             for (int e = tid; e < 16 * (D / 4); e += NT) {
                 const int r = e / (D / 4), c4 = e - r * (D / 4);
                 const int lr = mt * 16 + r;
@@ -520,10 +624,25 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                     const float mw = wave_m[w][lr];
                     ll += mw == -__builtin_inff() ? 0.f : wave_l[w][lr] * (mw == mm ? 1.f : exp2_fast(mw - mm));
                 }
+                const int row = row0 + lr;
+                const int node = min(row, p.rows - 1) / p.group;
+                if (any_odd) {
+#pragma unroll 1
+                    for (int j = 0; j <= p.k; ++j) {
+                        if (j > 0 && (node == 0 || !((anc[node - 1] >> (j - 1)) & 1))) continue;
+                        const int page = table[(len + j) >> p.page_shift];
+                        const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
+                        const uint64_t at = ((id * p.kv_heads + h) << p.page_shift) + ((len + j) & page_mask);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint16_t x = vc[at * D + c4 * 4 + i];
+                            if (nonfinite16<F16>(x)) o[i] += from16<F16>(x);
+                        }
+                    }
+                }
                 if (whole) {
-                    const int row = row0 + lr;
                     if (row < p.rows) {
-                        const int node = row / p.group, head = h * p.group + row - node * p.group;
+                        const int head = h * p.group + row - node * p.group;
                         const bool there = node == 0 || anc[node - 1] != 0;
                         const int64_t at = (static_cast<int64_t>(b) * (p.k + 1) + node) * p.q_heads + head;
                         const float inv = 1.f / ll;
