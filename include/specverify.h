@@ -549,7 +549,7 @@ sv_status sv_draft_len_update(sv_draft_len_ctl* ctl, const int32_t* hist, int32_
 typedef struct sv_tree_attention_desc {
     int32_t B;            /* sequences, in [0, 65535] */
     int32_t k;            /* draft nodes, in [0, 64]; 0: the root alone (plain decoding) */
-    int32_t q_heads;      /* a multiple of kv_heads, at most 1024 */
+    int32_t q_heads;      /* a multiple of kv_heads, at most 256 */
     int32_t kv_heads;     /* >= 1 */
     int32_t head_dim;     /* 64, 96, 128 or 256 */
     int32_t n_pages;      /* pages of the cache; n_pages * kv_heads * page_size < 2^32 */

@@ -12,17 +12,26 @@ namespace sv {
 
 // ---- attention of a tree over the paged cache --------------------------------
 
-// Workgroups of the attention kernel.  Each takes an equal share of the
-// batch's key tiles, so the count is also the number of partial-result slots
-// (two a workgroup) that the workspace holds.
-constexpr int kAttnWgs = 256;
+// Workgroups of the attention kernel: two for each of the 256 compute units,
+// so that one's loads go on while the other starts or ends a run of keys.
+constexpr int kAttnWgs = 512;
+constexpr int kAttnDies = 8;
 constexpr int kAttnStep = 32;  // keys one wavefront takes per step
 
 // Wavefronts per workgroup and row tiles of 16 query rows per workgroup: what
-// the staging buffers (160 KiB of LDS) and the accumulators (512 registers a
-// lane) hold.
-constexpr int attn_waves(int head_dim) { return head_dim > 128 ? 2 : 4; }
+// the staging buffers (160 KiB of LDS for two workgroups) and the accumulators
+// (512 registers a lane) hold.
+constexpr int attn_waves(int head_dim) { return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 4; }
 constexpr int attn_max_row_tiles(int head_dim) { return head_dim > 128 ? 2 : 4; }
+
+// A (sequence, key head) whose keys several clusters share, seen from the
+// first of them; k_tree_combine joins their partial results.
+struct AttnSplit {
+    int32_t b;      // -1: none starts here
+    int32_t head;   // key head
+    int32_t last;   // the last cluster that has part of it
+    int32_t slot1;  // the first cluster's part is in its second slot
+};
 
 struct AttnPlan {
     const void* q;
@@ -33,8 +42,9 @@ struct AttnPlan {
     const int32_t* parents;  // NULL when k == 0
     void* out;
     float* lse;              // may be NULL
-    float* part_acc;         // [slots][row_tiles * 16][head_dim]
-    float* part_ml;          // [slots][row_tiles * 16][2]
+    float* part_acc;         // [clusters][row_units][2 slots][row_tiles * 16][head_dim]
+    float* part_ml;          // the same [..][2]
+    AttnSplit* splits;       // [clusters][row_units]
     int64_t q_stride_b, q_stride_r, q_stride_h;
     int32_t batch;
     int32_t k;
@@ -43,6 +53,8 @@ struct AttnPlan {
     int32_t rows;            // (k + 1) * group: query rows of one key head
     int32_t row_tiles;       // 16-row tiles of one unit, 1 .. attn_max_row_tiles
     int32_t row_units;       // units that share one key head's rows
+    int32_t cluster;         // workgroups that take the same keys, a unit (or several, in turn) each
+    int32_t clusters;
     int32_t n_pages, page_shift, max_pages;
     int32_t is_f16;
     float scale_log2;        // scale * log2(e)

@@ -28,7 +28,7 @@ int page_shift_of(int32_t size) {
 sv_status plan_attention(const sv_tree_attention_desc* d, AttnPlan* p) {
     if (!d) return SV_ERR_NULL_ARG;
     if (d->B < 0 || d->B > 65535 || d->k < 0 || d->k > SV_MAX_DRAFT) return SV_ERR_BAD_SHAPE;
-    if (d->kv_heads < 1 || d->q_heads < 1 || d->q_heads > 1024 || d->q_heads % d->kv_heads) return SV_ERR_BAD_SHAPE;
+    if (d->kv_heads < 1 || d->q_heads < 1 || d->q_heads > 256 || d->q_heads % d->kv_heads) return SV_ERR_BAD_SHAPE;
     if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128 && d->head_dim != 256) return SV_ERR_BAD_SHAPE;
     const int shift = page_shift_of(d->page_size);
     if (shift < 0 || d->n_pages < 1 || d->max_pages < 1) return SV_ERR_BAD_SHAPE;
@@ -52,7 +52,10 @@ sv_status plan_attention(const sv_tree_attention_desc* d, AttnPlan* p) {
     const int units = (tiles + most - 1) / most;
     p->row_tiles = (tiles + units - 1) / units;
     p->row_units = (tiles + p->row_tiles - 1) / p->row_tiles;
-    if (static_cast<int64_t>(d->B) * d->kv_heads * p->row_units >= (int64_t{1} << 31)) return SV_ERR_BAD_SHAPE;
+    // The units of one key head read the same keys: a cluster of workgroups on one die, so that these pass its L2 once.
+    constexpr int per_die = kAttnWgs / kAttnDies;
+    p->cluster = p->row_units < per_die ? p->row_units : per_die;
+    p->clusters = kAttnDies * (per_die / p->cluster);
     p->n_pages = d->n_pages;
     p->page_shift = shift;
     p->max_pages = d->max_pages;
@@ -64,11 +67,15 @@ sv_status plan_attention(const sv_tree_attention_desc* d, AttnPlan* p) {
     return SV_OK;
 }
 
-size_t attention_slot_rows(const AttnPlan& p) { return static_cast<size_t>(kAttnWgs) * 2 * p.row_tiles * 16; }
+size_t attention_slot_rows(const AttnPlan& p) {
+    return static_cast<size_t>(p.clusters) * p.row_units * 2 * p.row_tiles * 16;
+}
+size_t attention_acc_bytes(const AttnPlan& p) { return align_up(attention_slot_rows(p) * p.head_dim * sizeof(float)); }
+size_t attention_ml_bytes(const AttnPlan& p) { return align_up(attention_slot_rows(p) * 2 * sizeof(float)); }
 
 size_t attention_bytes(const AttnPlan& p) {
-    return align_up(attention_slot_rows(p) * p.head_dim * sizeof(float)) +
-           align_up(attention_slot_rows(p) * 2 * sizeof(float));
+    return attention_acc_bytes(p) + attention_ml_bytes(p) +
+           align_up(static_cast<size_t>(p.clusters) * p.row_units * sizeof(AttnSplit));
 }
 
 // As many slices of whole tiles to a row as make about kTreeWgs workgroups on `rows` rows.
@@ -184,9 +191,10 @@ sv_status sv_tree_attention(const sv_tree_attention_desc* desc, const void* q, c
     p.parents = parents;
     p.out = out;
     p.lse = lse_out;
-    p.part_acc = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                         sv::align_up(sv::attention_slot_rows(p) * p.head_dim * sizeof(float)));
+    char* const base = static_cast<char*>(workspace);
+    p.part_acc = reinterpret_cast<float*>(base);
+    p.part_ml = reinterpret_cast<float*>(base + sv::attention_acc_bytes(p));
+    p.splits = reinterpret_cast<sv::AttnSplit*>(base + sv::attention_acc_bytes(p) + sv::attention_ml_bytes(p));
     return sv::launched(sv::launch_tree_attention(p, stream));
 }
 

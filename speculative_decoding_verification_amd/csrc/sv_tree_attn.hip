@@ -54,7 +54,6 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
 
 constexpr float kRaise = 8.f;  // log2 by which a score may pass the running maximum
-constexpr int kXcdCount = 8;
 
 template <bool F16>
 __device__ __forceinline__ floatx4_t mma(shortx8_t a, shortx8_t b, floatx4_t c) {
@@ -178,11 +177,13 @@ struct VReader {
     }
 };
 
-// Ancestors of draft node `lane` as a bit mask (itself included; 0 for an
+__device__ __forceinline__ int parent_of(const AttnPlan& p, int b, int lane) {
+    return lane < p.k ? p.parents[static_cast<int64_t>(b) * p.k + lane] : -2;
+}
+
+// Ancestors of draft node `lane`, of parent `up`, as a bit mask (itself included; 0 for an
 // absent node: parent -2, out of range, or absent itself), by doubling.
-__device__ __forceinline__ uint64_t ancestors(const AttnPlan& p, int b, int lane) {
-    int up = -2;
-    if (lane < p.k) up = p.parents[static_cast<int64_t>(b) * p.k + lane];
+__device__ __forceinline__ uint64_t ancestors(int up, int lane) {
     if (up >= lane || up < -2) up = -2;
     uint64_t mask = up == -2 ? 0 : (uint64_t{1} << lane);
     bool gone = up == -2;
@@ -231,18 +232,48 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t
     return v;
 }
 
-// Tiles of one (key head, row block) of the whole batch.
-template <int NT>
-__device__ int64_t batch_tiles(const AttnPlan& p, int tile_keys, int64_t* tmp) {
-    int64_t sum = 0, all;
-    for (int b = threadIdx.x; b < p.batch; b += NT) sum += seq_tiles(p, b, tile_keys);
-    block_scan<NT>(sum, &all, tmp);
-    return all;
-}
+// What a workgroup finds of the line of all sequences' key tiles, key head
+// by key head: its run, and where the run begins.
+struct Line {
+    int64_t begin, end, share;
+    int b;          // the sequence that `begin` lies in
+    int64_t b_off;  // the line's index of that sequence's first tile
+};
 
-__host__ __device__ inline int64_t share_of(int64_t total) {
-    const int64_t w = (total + kAttnWgs - 1) / kAttnWgs;
-    return w > 0 ? w : 1;
+template <int NT>
+__device__ __forceinline__ Line find_run(const AttnPlan& p, int cluster, int tile_keys, int64_t* tmp) {
+    __shared__ int64_t found_off;
+    __shared__ int found_b;
+    const int heads = p.kv_heads;
+    const bool once = p.batch <= NT;  // one scan has it all
+    int64_t mine = 0, sum = 0, total;
+    for (int b = threadIdx.x; b < p.batch; b += NT) sum += mine = seq_tiles(p, b, tile_keys);
+    int64_t incl = block_scan<NT>(sum, &total, tmp);
+    Line r;
+    total *= heads;
+    r.share = (total + p.clusters - 1) / p.clusters;
+    if (r.share < 1) r.share = 1;
+    r.begin = cluster * r.share;
+    r.end = min(r.begin + r.share, total);
+    if (r.begin >= r.end) return r;
+    int64_t base = 0;
+    for (int c = 0; base * heads <= r.begin; c += NT) {
+        int64_t all = total;
+        if (!once) {
+            mine = c + static_cast<int>(threadIdx.x) < p.batch ? seq_tiles(p, c + threadIdx.x, tile_keys) : 0;
+            incl = block_scan<NT>(mine, &all, tmp);
+        }
+        const int64_t before = base + incl - mine;
+        if (mine > 0 && r.begin >= before * heads && r.begin < (before + mine) * heads) {
+            found_b = c + threadIdx.x;
+            found_off = before * heads;
+        }
+        base += all;
+    }
+    __syncthreads();
+    r.b = found_b;
+    r.b_off = found_off;
+    return r;
 }
 
 template <bool F16, int D, int MT>
@@ -262,86 +293,66 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     constexpr int BUF = STEP * D;  // elements of one buffer
     __shared__ __attribute__((aligned(1024))) uint16_t stage[NW * 4 * BUF];
     __shared__ float wave_m[NW][MT * 16], wave_l[NW][MT * 16];
+    __shared__ int wave_odd[NW];  // whether the wavefront met a tree row's value that is not finite
     __shared__ uint64_t anc[SV_MAX_DRAFT];
     __shared__ int64_t scan_tmp[NW];
-    __shared__ int64_t first_off;
-    __shared__ int first_b;
-    __shared__ int wave_odd[NW];  // whether the wavefront met a tree row's value that is not finite
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // one value a wavefront: what follows from it stays scalar
     const int q_of = lane & 15, g = lane >> 4;
-    // Blocks are dealt to the eight dies in turn: neighbours in the line of
-    // tiles (row blocks of one key head among them) run on one die.
-    const int wg = (blockIdx.x % kXcdCount) * (kAttnWgs / kXcdCount) + blockIdx.x / kXcdCount;
-    const int per_seq = p.kv_heads * p.row_units;
-    const int64_t total = batch_tiles<NT>(p, TILE, scan_tmp) * per_seq;
-    const int64_t share = share_of(total);
-    int64_t pos = wg * share;
-    const int64_t end = min(pos + share, total);
-    if (pos >= end) return;
-    {
-        int64_t base = 0;
-        for (int c = 0; base * per_seq <= pos; c += NT) {
-            const int b = c + tid;
-            const int64_t v = b < p.batch ? seq_tiles(p, b, TILE) : 0;
-            int64_t all;
-            const int64_t before = base + block_scan<NT>(v, &all, scan_tmp) - v;
-            if (v > 0 && pos >= before * per_seq && pos < (before + v) * per_seq) {
-                first_b = b;
-                first_off = before * per_seq;
-            }
-            base += all;
-        }
-        __syncthreads();
-    }
-    int b = first_b;
-    int64_t seq_off = first_off;  // the line's index of sequence b's first tile
-    int nt = static_cast<int>(seq_tiles(p, b, TILE));
-    bool new_seq = true;
-
     const uint16_t* const kc = static_cast<const uint16_t*>(p.k_cache);
     const uint16_t* const vc = static_cast<const uint16_t*>(p.v_cache);
     const int page_mask = (1 << p.page_shift) - 1;
+    // Blocks are dealt to the eight dies in turn; a cluster's stand on one die.
+    const int on_die = blockIdx.x / kAttnDies, per_die = p.clusters / kAttnDies;
+    const int cluster = (blockIdx.x % kAttnDies) * per_die + on_die / p.cluster;
+    const bool works = on_die < per_die * p.cluster;
+    Line run{0, 0, 1, 0, 0};
+    if (works) run = find_run<NT>(p, cluster, TILE, scan_tmp);
 
-    while (pos < end) {
-        while (pos >= seq_off + static_cast<int64_t>(nt) * per_seq) {  // the next sequence that has tiles
-            seq_off += static_cast<int64_t>(nt) * per_seq;
+    for (int ru = on_die % p.cluster; works && ru < p.row_units; ru += p.cluster) {
+    int64_t pos = run.begin;
+    int b = run.b;
+    int64_t seq_off = run.b_off;  // the line's index of sequence b's first tile
+    AttnSplit split{-1, 0, 0, 0};
+    int nt = pos < run.end ? static_cast<int>(seq_tiles(p, b, TILE)) : 0;
+    while (pos < run.end) {
+        while (pos >= seq_off + static_cast<int64_t>(nt) * p.kv_heads) {  // the next sequence that has tiles
+            seq_off += static_cast<int64_t>(nt) * p.kv_heads;
             ++b;
             nt = static_cast<int>(seq_tiles(p, b, TILE));
-            new_seq = true;
-        }
-        if (new_seq) {
-            __syncthreads();  // the previous sequence's readers of anc are done
-            if (wave == 0) {
-                const uint64_t m = ancestors(p, b, lane);
-                anc[lane] = m;
-            }
-            __syncthreads();
-            new_seq = false;
         }
         const int64_t in_seq = pos - seq_off;
-        const int unit = static_cast<int>(in_seq / nt);
-        const int t0 = static_cast<int>(in_seq - static_cast<int64_t>(unit) * nt);
-        const int t1 = static_cast<int>(min<int64_t>(nt, t0 + (end - pos)));
-        const int h = unit / p.row_units;
-        const int row0 = (unit - h * p.row_units) * (MT * 16);
+        const int h = static_cast<int>(in_seq / nt);
+        const int64_t unit_off = seq_off + static_cast<int64_t>(h) * nt;
+        const int t0 = static_cast<int>(pos - unit_off);
+        const int t1 = static_cast<int>(min<int64_t>(nt, t0 + (run.end - pos)));
+        const int row0 = ru * (MT * 16);
         const int len = p.seq_len[b];
         const int keys = len + p.k + 1;
-        const uint64_t present = __ballot(anc[lane] != 0);
         const int32_t* const table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        const int up = parent_of(p, b, lane);
 
         shortx8_t qf[MT][KK];
-        uint64_t see[MT];  // the draft nodes that this lane's row sees
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int r = min(row0 + mt * 16 + q_of, p.rows - 1);
             const int node = r / p.group, head = h * p.group + r - node * p.group;
-            see[mt] = node == 0 ? 0 : anc[node - 1];
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(b) * p.q_stride_b +
                                   static_cast<int64_t>(node) * p.q_stride_r + static_cast<int64_t>(head) * p.q_stride_h;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
                 qf[mt][kk] = *reinterpret_cast<const shortx8_t*>(src + (kk * 4 + g) * 8);
+        }
+        const uint64_t own_mask = ancestors(up, lane);
+        const uint64_t present = __ballot(own_mask != 0);
+        if (wave == 0) anc[lane] = own_mask;  // (read after the barriers below)
+        uint64_t see[MT];  // the draft nodes that this lane's row sees
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int node = min(row0 + mt * 16 + q_of, p.rows - 1) / p.group;
+            const uint64_t m = __shfl(static_cast<unsigned long long>(own_mask), max(node - 1, 0));
+            see[mt] = node == 0 ? 0 : m;
         }
         floatx4_t acc[MT][DB];
         float m[MT], l[MT];
@@ -396,9 +407,11 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                         (__attribute__((address_space(3))) void*)(to + i * 512), 16, 0, 0);
                 }
             } else {
+                int ln = lane;
+                asm volatile("" : "+v"(ln));  // worked out where it is needed: hoisted, these offsets cost 32 registers
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    const int e = i * 64 + lane;
+                    const int e = i * 64 + ln;
                     const int r = e / CH, c = e - r * CH;
                     const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(row), r))) * D;
                     __builtin_amdgcn_global_load_lds((const void*)(cache + at + ((c ^ swizzle(r)) << 3)),
@@ -605,9 +618,12 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         int any_odd = 0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) any_odd |= wave_odd[w];
-        // A workgroup's first slot takes a run that it begins with, its second
-        // one that goes on in the next workgroup.
-        const int64_t slot = static_cast<int64_t>(wg) * 2 + (pos == wg * share ? 0 : 1);
+        // A cluster's first slot takes the keys that its run begins with, its
+        // second those that go on in the next run.
+        const int second = pos != run.begin;
+        const int64_t slot = (static_cast<int64_t>(cluster) * p.row_units + ru) * 2 + second;
+        if (t0 == 0 && !whole)
+            split = AttnSplit{b, h, static_cast<int>((unit_off + nt - 1) / run.share), second};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const float* const buf = reinterpret_cast<const float*>(stage) + mt * (NW * 16 * D);
@@ -665,74 +681,75 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         __syncthreads();  // the buffers are free again
         pos += steps;
     }
+    if (tid == 0) p.splits[static_cast<int64_t>(cluster) * p.row_units + ru] = split;
+    }
+    // Absent sequences have no tiles; their rows are zeros.
+    for (int b = blockIdx.x; b < p.batch; b += kAttnWgs) {
+        if (seq_tiles(p, b, TILE) > 0) continue;
+        const int64_t n = static_cast<int64_t>(p.k + 1) * p.q_heads;
+        for (int64_t e = tid; e < n * (D / 8); e += NT)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + b * n * D)[e] = uint4{0, 0, 0, 0};
+        if (p.lse)
+            for (int64_t e = tid; e < n; e += NT) p.lse[b * n + e] = -__builtin_inff();
+    }
 }
 
-// One workgroup of four wavefronts joins up to four rows of one unit.
-template <bool F16>
+// Joins the parts of what several clusters share: a wavefront for each row,
+// its lanes in groups of D / 4 that take the parts in turn.
+template <bool F16, int D>
 __global__ __launch_bounds__(256) void k_tree_combine(AttnPlan p) {
-    __shared__ int64_t scan_tmp[4];
-    __shared__ uint64_t anc[SV_MAX_DRAFT];
-    const int tile_keys = attn_waves(p.head_dim) * kAttnStep;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int per_seq = p.kv_heads * p.row_units;
-    const int b = blockIdx.x / per_seq;
-    const int unit = blockIdx.x - b * per_seq;
-    const int64_t total = batch_tiles<256>(p, tile_keys, scan_tmp) * per_seq;
-    const int64_t share = share_of(total);
-    int64_t before = 0;
-    for (int i = tid; i < b; i += 256) before += seq_tiles(p, i, tile_keys);
-    int64_t all;
-    block_scan<256>(before, &all, scan_tmp);
-    const int64_t nt = seq_tiles(p, b, tile_keys);
-    const int64_t off = all * per_seq + unit * nt;
-    const int64_t w0 = off / share, w1 = nt > 0 ? (off + nt - 1) / share : w0 - 1;
-    if (w0 == w1) return;  // one workgroup held all of it
-    if (wave == 0) {
-        const uint64_t m = ancestors(p, b, lane);
-        anc[lane] = m;
-    }
-    __syncthreads();
-    const int D = p.head_dim;
+    const int cluster = blockIdx.x / p.row_units, ru = blockIdx.x - cluster * p.row_units;
+    const AttnSplit s = p.splits[blockIdx.x];
+    if (s.b < 0) return;
+    constexpr int LANES = D / 4, GROUPS = 64 / LANES;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int unit_rows = p.row_tiles * 16;
-    const int h = unit / p.row_units;
     const int lr = blockIdx.y * 4 + wave;
-    const int row = (unit - h * p.row_units) * unit_rows + lr;
+    const int row = ru * unit_rows + lr;
     if (row >= p.rows) return;
-    const int node = row / p.group, head = h * p.group + row - node * p.group;
-    const int64_t at = (static_cast<int64_t>(b) * (p.k + 1) + node) * p.q_heads + head;
-    uint16_t* const out = static_cast<uint16_t*>(p.out) + at * D;
-    const bool there = nt > 0 && (node == 0 || anc[node - 1] != 0);
-    const int c = lane * 4;  // a lane takes four columns
-    if (!there) {
-        if (c < D) *reinterpret_cast<shortx4_t*>(out + c) = shortx4_t{0, 0, 0, 0};
-        if (p.lse && lane == 0) p.lse[at] = -__builtin_inff();
-        return;
-    }
-    const auto slot_row = [&](int64_t w) {
-        const int64_t slot = w * 2 + (w == w0 && off > w * share ? 1 : 0);
+    const int node = row / p.group, head = s.head * p.group + row - node * p.group;
+    const int64_t at = (static_cast<int64_t>(s.b) * (p.k + 1) + node) * p.q_heads + head;
+    const uint64_t mask = ancestors(parent_of(p, s.b, lane), lane);
+    const uint64_t there_mask = __ballot(mask != 0);
+    const bool there = node == 0 || ((there_mask >> (node - 1)) & 1);
+    const int count = s.last - cluster + 1;
+    const auto slot_row = [&](int i) {
+        const int64_t slot = (static_cast<int64_t>(cluster + i) * p.row_units + ru) * 2 + (i == 0 ? s.slot1 : 0);
         return slot * unit_rows + lr;
     };
     float mm = -__builtin_inff();
-    for (int64_t w = w0 + lane; w <= w1; w += 64) mm = fmaxf(mm, p.part_ml[slot_row(w) * 2]);
+    for (int i = lane; i < count; i += 64) mm = fmaxf(mm, p.part_ml[slot_row(i) * 2]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+    const int group = lane / LANES, c = (lane - group * LANES) * 4;
     float ll = 0.f;
     floatx4_t o{0.f, 0.f, 0.f, 0.f};
-    for (int64_t w = w0; w <= w1; ++w) {
-        const int64_t r = slot_row(w);
-        const float mw = p.part_ml[r * 2], lw = p.part_ml[r * 2 + 1];
-        const float a = mw == -__builtin_inff() ? 0.f : (mw == mm ? 1.f : exp2_fast(mw - mm));
-        ll += lw * a;
-        if (c < D) o += *reinterpret_cast<const floatx4_t*>(p.part_acc + r * D + c) * a;
+    if (group < GROUPS) {
+#pragma unroll 4
+        for (int i = group; i < count; i += GROUPS) {
+            const int64_t r = slot_row(i);
+            const float mw = p.part_ml[r * 2], lw = p.part_ml[r * 2 + 1];
+            const float a = mw == -__builtin_inff() ? 0.f : (mw == mm ? 1.f : exp2_fast(mw - mm));
+            ll += lw * a;
+            o += *reinterpret_cast<const floatx4_t*>(p.part_acc + r * D + c) * a;
+        }
     }
-    const float inv = 1.f / ll;
-    if (c < D) {
-        shortx4_t x;
+    const float l0 = ll;
+    const floatx4_t o0 = o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = to16<F16>(o[i] * inv);
-        *reinterpret_cast<shortx4_t*>(out + c) = x;
+    for (int q = 1; q < GROUPS; ++q) {  // the groups' sums, in order
+        const int from = (lane + q * LANES) & 63;
+        ll += __shfl(l0, from);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += __shfl(o0[i], from);
     }
-    if (p.lse && lane == 0) p.lse[at] = (mm + __log2f(ll)) * 0.69314718055994531f;
+    if (lane >= LANES) return;
+    const float inv = 1.f / ll;
+    shortx4_t x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = there ? to16<F16>(o[i] * inv) : short{0};
+    *reinterpret_cast<shortx4_t*>(static_cast<uint16_t*>(p.out) + at * D + c) = x;
+    if (p.lse && lane == 0) p.lse[at] = there ? (mm + __log2f(ll)) * 0.69314718055994531f : -__builtin_inff();
 }
 
 template <bool F16, int D>
@@ -748,22 +765,20 @@ hipError_t launch_d(const AttnPlan& p, hipStream_t stream) {
             if constexpr (attn_max_row_tiles(D) >= 4) k_tree_attn<F16, D, 4><<<grid, block, 0, stream>>>(p);
             break;
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_tree_combine<F16, D><<<dim3(p.clusters * p.row_units, p.row_tiles * 4), dim3(256), 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <bool F16>
 hipError_t launch_t(const AttnPlan& p, hipStream_t stream) {
-    hipError_t e;
     switch (p.head_dim) {
-        case 64: e = launch_d<F16, 64>(p, stream); break;
-        case 96: e = launch_d<F16, 96>(p, stream); break;
-        case 128: e = launch_d<F16, 128>(p, stream); break;
-        default: e = launch_d<F16, 256>(p, stream); break;
+        case 64: return launch_d<F16, 64>(p, stream);
+        case 96: return launch_d<F16, 96>(p, stream);
+        case 128: return launch_d<F16, 128>(p, stream);
+        default: return launch_d<F16, 256>(p, stream);
     }
-    if (e != hipSuccess) return e;
-    const dim3 grid(static_cast<uint32_t>(p.batch) * p.kv_heads * p.row_units, p.row_tiles * 4);
-    k_tree_combine<F16><<<grid, dim3(256), 0, stream>>>(p);
-    return hipGetLastError();
 }
 
 }  // namespace
