@@ -107,75 +107,186 @@ __device__ __forceinline__ int swizzle_v(int r) {
     return (2 * r) & 15;
 }
 
-// The staged operands are read in inline assembly that waits for what it
-// reads: the compiler cannot tell a transposing read from the loads in flight
-// to the other buffers and would wait for all of them.  A K read takes the
-// lane's pieces kk of its row, a V read four keys of one column in each half
-// of the step.  `half` is the byte offset of the step's second 16 rows.
+// Byte addresses of a lane's staged operands: piece kk of K's row, and for
+// each block of 16 columns four keys of V's column (the transposing read wants
+// the address of the piece that the lane brings in, not of its result).  For
+// the powers of two the swizzle is an exclusive or of the address; for head
+// size 96 it adds `odd` to even column blocks and takes it from odd ones.
 template <int D>
-struct KReader {  // byte address of piece kk: for powers of two the swizzle is an exclusive or of the address
+struct KAddress {
     uint32_t base;
-    __device__ __forceinline__ KReader(uint32_t lds, int row, int g) {
+    __device__ __forceinline__ KAddress(uint32_t lds, int row, int g) {
         base = lds + row * (D * 2) + ((g ^ swizzle_k<D>(row)) << 4);
     }
-    __device__ __forceinline__ uint32_t at(int kk) const { return D == 96 ? base + kk * 64 : base ^ (kk << 6); }
-    template <int HALF>
-    __device__ __forceinline__ void read(shortx8_t (&a)[D / 32]) const {
-        constexpr int off = HALF * 16 * D * 2;
-        if constexpr (D == 64)
-            asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
-                         : "=&v"(a[0]), "=&v"(a[1]) : "v"(at(0)), "v"(at(1)), "n"(off) : "memory");
-        else if constexpr (D == 96)
-            asm volatile("ds_read_b128 %0, %3 offset:%4\n\tds_read_b128 %1, %3 offset:%5\n\t"
-                         "ds_read_b128 %2, %3 offset:%6\n\ts_waitcnt lgkmcnt(0)"
-                         : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2])
-                         : "v"(base), "n"(off), "n"(off + 64), "n"(off + 128) : "memory");
-        else
-#pragma unroll
-            for (int i = 0; i < D / 32; i += 4)
-                asm volatile("ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
-                             "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
-                             : "=&v"(a[i]), "=&v"(a[i + 1]), "=&v"(a[i + 2]), "=&v"(a[i + 3])
-                             : "v"(at(i)), "v"(at(i + 1)), "v"(at(i + 2)), "v"(at(i + 3)), "n"(off) : "memory");
-    }
+    __device__ __forceinline__ uint32_t at(int kk) const { return base ^ (kk << 6); }
 };
 
 template <int D>
-struct VReader {
-    static constexpr int N = D == 96 ? 3 : 4;  // column blocks of 16 that one read takes
+struct VAddress {
     uint32_t base;
-    int odd;  // head size 96: what the swizzle adds to even blocks and takes from odd ones
-    __device__ __forceinline__ VReader(uint32_t lds, int lane) {
+    uint32_t odd;
+    __device__ __forceinline__ VAddress(uint32_t lds, int lane) {
         const int i = lane & 15, r = (lane >> 4) * 4 + (i >> 2), pair = (i & 3) >> 1, sw = swizzle_v<D>(r);
-        if constexpr (D == 96) {
-            odd = (sw >> 1) * 32;
-            base = lds + r * (D * 2) + pair * 16 + (i & 1) * 8;
-        } else {
-            odd = 0;
-            base = lds + r * (D * 2) + ((pair ^ sw) << 4) + (i & 1) * 8;
-        }
+        odd = D == 96 ? (sw >> 1) * 32 : 0;
+        base = lds + r * (D * 2) + (D == 96 ? pair * 16 : (pair ^ sw) << 4) + (i & 1) * 8;
     }
-    __device__ __forceinline__ uint32_t at(int db) const {
-        return D == 96 ? base + db * 32 + (db & 1 ? -odd : odd) : base ^ (db << 5);
-    }
-    __device__ __forceinline__ void read(int db, shortx4_t (&lo)[N], shortx4_t (&hi)[N]) const {
-        constexpr int half = 16 * D * 2;
-        if constexpr (N == 3)
-            asm volatile("ds_read_b64_tr_b16 %0, %6\n\tds_read_b64_tr_b16 %1, %6 offset:%9\n\t"
-                         "ds_read_b64_tr_b16 %2, %7\n\tds_read_b64_tr_b16 %3, %7 offset:%9\n\t"
-                         "ds_read_b64_tr_b16 %4, %8\n\tds_read_b64_tr_b16 %5, %8 offset:%9\n\ts_waitcnt lgkmcnt(0)"
-                         : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2])
-                         : "v"(at(db)), "v"(at(db + 1)), "v"(at(db + 2)), "n"(half) : "memory");
-        else
-            asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %4, %10\n\tds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %6, %11\n\tds_read_b64_tr_b16 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
-                         : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]),
-                           "=&v"(lo[3]), "=&v"(hi[3])
-                         : "v"(at(db)), "v"(at(db + 1)), "v"(at(db + 2)), "v"(at(db + 3)), "n"(half) : "memory");
-    }
+    __device__ __forceinline__ uint32_t at(int db) const { return base ^ (db << 5); }
 };
+
+// All of a step's reads in one piece of assembly that waits for them: the
+// compiler cannot tell a transposing read from the loads in flight to the other
+// buffers and would wait for all of these too.  a[kb][kk]: K, 16 keys kb; lo,
+// hi[db]: V, the first and second 16 keys.
+template <int D>
+__device__ __forceinline__ void read_step(const KAddress<D>& k, const VAddress<D>& v, shortx8_t (&a)[2][D / 32],
+                                          shortx4_t (&lo)[D / 16], shortx4_t (&hi)[D / 16]) {
+    if constexpr (D == 64)
+        asm volatile(
+                     "ds_read_b128 %0, %12 offset:0\n\t"
+                     "ds_read_b128 %1, %13 offset:0\n\t"
+                     "ds_read_b128 %2, %12 offset:2048\n\t"
+                     "ds_read_b128 %3, %13 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %4, %14 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %5, %14 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %6, %15 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %7, %15 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %8, %16 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %9, %16 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %10, %17 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %11, %17 offset:2048\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[1][0]), "=&a"(a[1][1]), "=&v"(lo[0]), "=&v"(hi[0]),
+                       "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3])
+                     : "v"(k.at(0)), "v"(k.at(1)), "v"(v.at(0)), "v"(v.at(1)), "v"(v.at(2)), "v"(v.at(3))
+                     : "memory");
+    else if constexpr (D == 96)
+        asm volatile(
+                     "ds_read_b128 %0, %18 offset:0\n\t"
+                     "ds_read_b128 %1, %18 offset:64\n\t"
+                     "ds_read_b128 %2, %18 offset:128\n\t"
+                     "ds_read_b128 %3, %18 offset:3072\n\t"
+                     "ds_read_b128 %4, %18 offset:3136\n\t"
+                     "ds_read_b128 %5, %18 offset:3200\n\t"
+                     "ds_read_b64_tr_b16 %6, %19 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %7, %19 offset:3072\n\t"
+                     "ds_read_b64_tr_b16 %8, %20 offset:32\n\t"
+                     "ds_read_b64_tr_b16 %9, %20 offset:3104\n\t"
+                     "ds_read_b64_tr_b16 %10, %19 offset:64\n\t"
+                     "ds_read_b64_tr_b16 %11, %19 offset:3136\n\t"
+                     "ds_read_b64_tr_b16 %12, %20 offset:96\n\t"
+                     "ds_read_b64_tr_b16 %13, %20 offset:3168\n\t"
+                     "ds_read_b64_tr_b16 %14, %19 offset:128\n\t"
+                     "ds_read_b64_tr_b16 %15, %19 offset:3200\n\t"
+                     "ds_read_b64_tr_b16 %16, %20 offset:160\n\t"
+                     "ds_read_b64_tr_b16 %17, %20 offset:3232\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[0][2]), "=&a"(a[1][0]), "=&a"(a[1][1]),
+                       "=&a"(a[1][2]), "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]),
+                       "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]),
+                       "=&v"(hi[5])
+                     : "v"(k.base), "v"(v.base + v.odd), "v"(v.base - v.odd)
+                     : "memory");
+    else if constexpr (D == 128)
+        asm volatile(
+                     "ds_read_b128 %0, %24 offset:0\n\t"
+                     "ds_read_b128 %1, %25 offset:0\n\t"
+                     "ds_read_b128 %2, %26 offset:0\n\t"
+                     "ds_read_b128 %3, %27 offset:0\n\t"
+                     "ds_read_b128 %4, %24 offset:4096\n\t"
+                     "ds_read_b128 %5, %25 offset:4096\n\t"
+                     "ds_read_b128 %6, %26 offset:4096\n\t"
+                     "ds_read_b128 %7, %27 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %8, %28 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %9, %28 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %10, %29 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %11, %29 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %12, %30 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %13, %30 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %14, %31 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %15, %31 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %16, %32 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %17, %32 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %18, %33 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %19, %33 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %20, %34 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %21, %34 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %22, %35 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %23, %35 offset:4096\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[0][2]), "=&a"(a[0][3]), "=&a"(a[1][0]),
+                       "=&a"(a[1][1]), "=&a"(a[1][2]), "=&a"(a[1][3]), "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]),
+                       "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]),
+                       "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]), "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]),
+                       "=&v"(hi[7])
+                     : "v"(k.at(0)), "v"(k.at(1)), "v"(k.at(2)), "v"(k.at(3)), "v"(v.at(0)), "v"(v.at(1)),
+                       "v"(v.at(2)), "v"(v.at(3)), "v"(v.at(4)), "v"(v.at(5)), "v"(v.at(6)), "v"(v.at(7))
+                     : "memory");
+    else
+        asm volatile(
+                     "ds_read_b128 %0, %48 offset:0\n\t"
+                     "ds_read_b128 %1, %49 offset:0\n\t"
+                     "ds_read_b128 %2, %50 offset:0\n\t"
+                     "ds_read_b128 %3, %51 offset:0\n\t"
+                     "ds_read_b128 %4, %52 offset:0\n\t"
+                     "ds_read_b128 %5, %53 offset:0\n\t"
+                     "ds_read_b128 %6, %54 offset:0\n\t"
+                     "ds_read_b128 %7, %55 offset:0\n\t"
+                     "ds_read_b128 %8, %48 offset:8192\n\t"
+                     "ds_read_b128 %9, %49 offset:8192\n\t"
+                     "ds_read_b128 %10, %50 offset:8192\n\t"
+                     "ds_read_b128 %11, %51 offset:8192\n\t"
+                     "ds_read_b128 %12, %52 offset:8192\n\t"
+                     "ds_read_b128 %13, %53 offset:8192\n\t"
+                     "ds_read_b128 %14, %54 offset:8192\n\t"
+                     "ds_read_b128 %15, %55 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %16, %56 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %17, %56 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %18, %57 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %19, %57 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %20, %58 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %21, %58 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %22, %59 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %23, %59 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %24, %60 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %25, %60 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %26, %61 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %27, %61 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %28, %62 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %29, %62 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %30, %63 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %31, %63 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %32, %64 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %33, %64 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %34, %65 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %35, %65 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %36, %66 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %37, %66 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %38, %67 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %39, %67 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %40, %68 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %41, %68 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %42, %69 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %43, %69 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %44, %70 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %45, %70 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %46, %71 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %47, %71 offset:8192\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[0][2]), "=&a"(a[0][3]), "=&a"(a[0][4]),
+                       "=&a"(a[0][5]), "=&a"(a[0][6]), "=&a"(a[0][7]), "=&a"(a[1][0]), "=&a"(a[1][1]),
+                       "=&a"(a[1][2]), "=&a"(a[1][3]), "=&a"(a[1][4]), "=&a"(a[1][5]), "=&a"(a[1][6]),
+                       "=&a"(a[1][7]), "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]),
+                       "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]),
+                       "=&v"(hi[5]), "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]), "=&v"(hi[7]), "=&v"(lo[8]),
+                       "=&v"(hi[8]), "=&v"(lo[9]), "=&v"(hi[9]), "=&v"(lo[10]), "=&v"(hi[10]), "=&v"(lo[11]),
+                       "=&v"(hi[11]), "=&v"(lo[12]), "=&v"(hi[12]), "=&v"(lo[13]), "=&v"(hi[13]), "=&v"(lo[14]),
+                       "=&v"(hi[14]), "=&v"(lo[15]), "=&v"(hi[15])
+                     : "v"(k.at(0)), "v"(k.at(1)), "v"(k.at(2)), "v"(k.at(3)), "v"(k.at(4)), "v"(k.at(5)),
+                       "v"(k.at(6)), "v"(k.at(7)), "v"(v.at(0)), "v"(v.at(1)), "v"(v.at(2)), "v"(v.at(3)),
+                       "v"(v.at(4)), "v"(v.at(5)), "v"(v.at(6)), "v"(v.at(7)), "v"(v.at(8)), "v"(v.at(9)),
+                       "v"(v.at(10)), "v"(v.at(11)), "v"(v.at(12)), "v"(v.at(13)), "v"(v.at(14)), "v"(v.at(15))
+                     : "memory");
+}
 
 __device__ __forceinline__ int parent_of(const AttnPlan& p, int b, int lane) {
     return lane < p.k ? p.parents[static_cast<int64_t>(b) * p.k + lane] : -2;
@@ -327,7 +438,9 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         const int64_t unit_off = seq_off + static_cast<int64_t>(h) * nt;
         const int t0 = static_cast<int>(pos - unit_off);
         const int t1 = static_cast<int>(min<int64_t>(nt, t0 + (run.end - pos)));
-        const int row0 = ru * (MT * 16);
+        int row0 = ru * (MT * 16);
+        asm volatile("" : "+s"(row0));  // what follows from it is worked out in place: hoisted out of the loop over the
+                                        // key heads it would hold registers through the steps
         const int len = p.seq_len[b];
         const int keys = len + p.k + 1;
         const int32_t* const table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
@@ -371,8 +484,8 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         uint16_t* const mine = stage + wave * (4 * BUF);
         const uint32_t lds = static_cast<uint32_t>(
             reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t*)mine));
-        const KReader<D> kread(lds, q_of, g);
-        const VReader<D> vread(lds + 2 * BUF * 2, lane);
+        const KAddress<D> k_at(lds, q_of, g);
+        const VAddress<D> v_at(lds + 2 * BUF * 2, lane);
         // Row of the cache (of head_dim elements) for the position that lane
         // (mod 32) stands for in step s.  Positions past the last key, and slots
         // of absent nodes, may hold anything (a NaN would spoil a product even
@@ -421,23 +534,15 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         };
         const auto k_dma = [&](int s, uint32_t row) { dma(kc, mine + (s & 1) * BUF, s, row, swizzle_k<D>); };
         const auto v_dma = [&](int s, uint32_t row) { dma(vc, mine + (2 + (s & 1)) * BUF, s, row, swizzle_v<D>); };
-        // Scores of step s, transposed: lane's row q_of, keys 16 kb + 4 g + i.
-        const auto scores = [&](int s, floatx4_t (&sc)[MT][2]) {
-            KReader<D> k = kread;
-            k.base += (s & 1) * (BUF * 2);
-            shortx8_t a[KK];
-            k.template read<0>(a);
+        // Scores of 32 keys, transposed: lane's row q_of, keys 16 kb + 4 g + i.
+        const auto scores = [&](const shortx8_t (&a)[2][KK], floatx4_t (&sc)[MT][2]) {
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    sc[mt][0] = mma<F16>(a[kk], qf[mt][kk], kk ? sc[mt][0] : floatx4_t{0.f, 0.f, 0.f, 0.f});
-            k.template read<1>(a);
+                for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    sc[mt][1] = mma<F16>(a[kk], qf[mt][kk], kk ? sc[mt][1] : floatx4_t{0.f, 0.f, 0.f, 0.f});
+                    for (int mt = 0; mt < MT; ++mt)
+                        sc[mt][kb] = mma<F16>(a[kb][kk], qf[mt][kk], kk ? sc[mt][kb] : floatx4_t{0.f, 0.f, 0.f, 0.f});
         };
         // The scores that a row's ancestry hides become -inf.
         const auto hide = [&](int s, floatx4_t (&sc)[MT][2]) {
@@ -457,65 +562,48 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                     sc[mt][i >> 2][i & 3] = (seen >> i) & 1 ? sc[mt][i >> 2][i & 3] : -__builtin_inff();
             }
         };
-        // Raises the maxima where a score passes them by 2^kRaise.
-        const auto raise_to = [&](const floatx4_t (&sc)[MT][2]) {
-            bool raise = false;
-            float top[MT];
+        // Whether a score passes its row's maximum by 2^kRaise; raise() then
+        // takes the maxima up to it.  The sums are rescaled outside the loop
+        // over steps that need it not: a branch over them inside made the
+        // compiler copy all accumulators at every step.
+        const auto top_of = [&](const floatx4_t (&sc)[MT][2], int mt) {
+            float t = sc[mt][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) t = fmaxf(t, sc[mt][i >> 2][i & 3]);
+            return t * p.scale_log2;
+        };
+        const auto past = [&](const floatx4_t (&sc)[MT][2]) {
+            bool any = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) any = any || top_of(sc, mt) > m[mt] + kRaise;
+            return __any(any) != 0;
+        };
+        const auto raise = [&](const floatx4_t (&sc)[MT][2]) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float t = sc[mt][0][0];
+                float t = top_of(sc, mt);
+                t = fmaxf(t, __shfl_xor(t, 16));
+                t = fmaxf(t, __shfl_xor(t, 32));
+                const float mn = fmaxf(m[mt], t);
+                const float f = m[mt] == mn ? 1.f : exp2_fast(m[mt] - mn);
+                m[mt] = mn;
+                l[mt] *= f;
 #pragma unroll
-                for (int i = 1; i < 8; ++i) t = fmaxf(t, sc[mt][i >> 2][i & 3]);
-                top[mt] = t * p.scale_log2;
-                raise = raise || top[mt] > m[mt] + kRaise;
-            }
-            if (__any(raise)) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float t = fmaxf(top[mt], __shfl_xor(top[mt], 16));
-                    t = fmaxf(t, __shfl_xor(t, 32));
-                    const float mn = fmaxf(m[mt], t);
-                    const float a = m[mt] == mn ? 1.f : exp2_fast(m[mt] - mn);
-                    m[mt] = mn;
-                    l[mt] *= a;
-#pragma unroll
-                    for (int db = 0; db < DB; ++db) acc[mt][db] *= a;
-                }
+                for (int db = 0; db < DB; ++db) acc[mt][db] *= f;
             }
         };
-        const auto weights = [&](const floatx4_t (&sc)[MT][2], shortx8_t (&pf)[MT]) {
+        const auto weights = [&](int mt, const floatx4_t (&sc)[MT][2]) {
+            const float ms = m[mt] == -__builtin_inff() ? 0.f : m[mt];
+            shortx8_t pf;
+            float sum = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const float ms = m[mt] == -__builtin_inff() ? 0.f : m[mt];
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float w = exp2_fast(__builtin_fmaf(sc[mt][i >> 2][i & 3], p.scale_log2, -ms));
-                    sum += w;
-                    pf[mt][i] = to16<F16>(w);
-                }
-                l[mt] += sum;
+            for (int i = 0; i < 8; ++i) {
+                const float w = exp2_fast(__builtin_fmaf(sc[mt][i >> 2][i & 3], p.scale_log2, -ms));
+                sum += w;
+                pf[i] = to16<F16>(w);
             }
-        };
-        // Key slot j of the product's lane group g is key 4g + j of the first
-        // 16 keys, for j >= 4 key 4g + j - 4 of the second: the weights stand so
-        // already, and the transposing read gives each lane four keys of one
-        // column.
-        const auto values = [&](int s, const shortx8_t (&pf)[MT]) {
-            VReader<D> v = vread;
-            v.base += (s & 1) * (BUF * 2);
-            constexpr int N = VReader<D>::N;
-#pragma unroll
-            for (int db = 0; db < DB; db += N) {
-                shortx4_t lo[N], hi[N];
-                v.read(db, lo, hi);
-#pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const shortx8_t a = __builtin_shufflevector(lo[n], hi[n], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) acc[mt][db + n] = mma<F16>(a, pf[mt], acc[mt][db + n]);
-                }
-            }
+            l[mt] += sum;
+            return pf;
         };
         // A value that is not finite must reach only the rows that see its
         // node, and the matrix product would multiply it by the other rows'
@@ -534,11 +622,12 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         };
 
         // While step s is worked on, the scores of step s + 1 are formed (its K
-        // has landed), K of step s + 2 and V of steps s + 1 and s + 2 are on
-        // their way.  Page numbers are asked for one step ahead of the rows.
+        // has landed), and K of steps s + 2 and s + 3 and V of steps s + 1 and
+        // s + 2 are on their way: a buffer is filled again as soon as it has
+        // been read.  Page numbers are asked for one step ahead of the rows.
         // Past the last step the loads repeat its rows, so that the count of
         // loads in flight is the same at every wait.
-        constexpr int kOne = NL, kTwo = 2 * NL;
+        constexpr int kTwo = 2 * NL;
         const auto landed = [&](auto left) {  // all but the last `left` loads
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0x0F70 | (decltype(left)::value & 15) | ((decltype(left)::value >> 4) << 14));
@@ -546,71 +635,113 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             __builtin_amdgcn_sched_barrier(0);
         };
         floatx4_t sc[MT][2], next[MT][2];
-        uint32_t row;
+        shortx8_t a[2][KK];
+        shortx4_t lo[DB], hi[DB];
+        const auto read = [&](int s) {  // K of step s, V of step s - 1
+            KAddress<D> k = k_at;
+            VAddress<D> v = v_at;
+            k.base += (s & 1) * (BUF * 2);
+            v.base += (~s & 1) * (BUF * 2);
+            read_step<D>(k, v, a, lo, hi);
+        };
+        uint32_t row_v, row_k;  // of steps s + 2 and s + 3
         {
-            const int pa = page_load(0), pb = page_load(1), pc = page_load(2);
-            row = row_of(0, pa);
-            k_dma(0, row);
-            v_dma(0, row);
-            row = row_of(1, pb);
-            k_dma(1, row);
+            const int pa = page_load(0), pb = page_load(1), pc = page_load(2), pd = page_load(3);
+            const uint32_t r0 = row_of(0, pa), r1 = row_of(1, pb);
+            k_dma(0, r0);
+            k_dma(1, r1);
+            v_dma(0, r0);
             landed(std::integral_constant<int, kTwo>{});
-            scores(0, sc);
-            v_dma(1, row);
-            row = row_of(2, pc);
+            read(0);  // (nothing of V yet)
+            scores(a, sc);
+            row_v = row_of(2, pc);
+            k_dma(2, row_v);
+            v_dma(1, r1);
+            row_k = row_of(3, pd);
         }
-        for (int s = 0; s < steps; ++s) {
-            landed(std::integral_constant<int, kOne>{});
+        // Steps that hold any key for this wavefront.
+        const int mine_n = min(steps, max(0, (keys - wave * STEP + STEP - 1) / STEP + NW - 1) / NW - t0);
+        const auto step = [&](int s, floatx4_t (&sc)[MT][2], floatx4_t (&next)[MT][2]) {
+            landed(std::integral_constant<int, kTwo>{});
             const bool tail = s >= full;
-            if (tail && key_of(s) >= keys) break;  // nothing of this wavefront's is left
-            if (tail) {
-                hide(s, sc);
-                clear_odd(s);
-            }
-            raise_to(sc);
-            const int page = page_load(s + 3);
-            k_dma(s + 2, row);
+            if (tail) clear_odd(s);
+            read(s + 1);
+            const int page = page_load(s + 4);
+            k_dma(s + 3, row_k);
+            v_dma(s + 2, row_v);
             __builtin_amdgcn_sched_barrier(0);
-            shortx8_t pf[MT];
-            scores(s + 1, next);
-            weights(sc, pf);
-            values(s, pf);
-            __builtin_amdgcn_sched_barrier(0);
-            v_dma(s + 2, row);
-            row = row_of(s + 3, page);
+            // One block without branches or memory: the next step's scores and
+            // this one's products on the matrix cores, its weights beside them.
+            scores(a, next);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                sc[mt][0] = next[mt][0];
-                sc[mt][1] = next[mt][1];
+                // Key slot j of the product's lane group g is key 4g + j of the
+                // first 16 keys, for j >= 4 key 4g + j - 4 of the second: the
+                // weights stand so already, and the transposing read gave each
+                // lane four keys of one column.
+                const shortx8_t pf = weights(mt, sc);
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+                    acc[mt][db] = mma<F16>(__builtin_shufflevector(lo[db], hi[db], 0, 1, 2, 3, 4, 5, 6, 7), pf, acc[mt][db]);
             }
+#pragma unroll
+            for (int i = 0; i < MT * (2 * KK + DB); ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // two vector ones
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            row_v = row_k;
+            row_k = row_of(s + 4, page);
+            if (s + 1 >= full) hide(s + 1, next);
+        };
+        if (full <= 0) hide(0, sc);
+        for (int s = 0; s < mine_n;) {
+            raise(sc);
+            bool more;
+            do {
+                step(s++, sc, next);
+                if (s >= mine_n || past(next)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        sc[mt][0] = next[mt][0];
+                        sc[mt][1] = next[mt][1];
+                    }
+                    break;
+                }
+                step(s++, next, sc);
+                more = s < mine_n && !past(sc);
+            } while (more);
         }
         __builtin_amdgcn_s_waitcnt(0x0F70);  // no load may land in a buffer that holds sums
         asm volatile("" ::: "memory");
 
         // Join the wavefronts.
+        int thread = tid;
+        asm volatile("" : "+v"(thread), "+s"(row0));  // as above
+        const int q_at = thread & 15, g_at = (thread & 63) >> 4;
         odd = __any(odd);
         if (lane == 0) wave_odd[wave] = odd;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float t = l[mt] + __shfl_xor(l[mt], 16);
             t += __shfl_xor(t, 32);
-            if (g == 0) {
-                wave_m[wave][mt * 16 + q_of] = m[mt];
-                wave_l[wave][mt * 16 + q_of] = t;
+            if (g_at == 0) {
+                wave_m[wave][mt * 16 + q_at] = m[mt];
+                wave_l[wave][mt * 16 + q_at] = t;
             }
         }
         __syncthreads();  // and every wavefront has left the buffers
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            float mm = wave_m[0][mt * 16 + q_of];
+            float mm = wave_m[0][mt * 16 + q_at];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][mt * 16 + q_of]);
+            for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][mt * 16 + q_at]);
             const float a = m[mt] == -__builtin_inff() ? 0.f : (m[mt] == mm ? 1.f : exp2_fast(m[mt] - mm));
             float* const buf = reinterpret_cast<float*>(stage) + mt * (NW * 16 * D);
 #pragma unroll
             for (int db = 0; db < DB; ++db) {
-                const int c = (db * 4 + g) ^ (q_of & 7);
-                *reinterpret_cast<floatx4_t*>(buf + (wave * 16 + q_of) * D + c * 4) = acc[mt][db] * a;
+                const int c = (db * 4 + g_at) ^ (q_at & 7);
+                *reinterpret_cast<floatx4_t*>(buf + (wave * 16 + q_at) * D + c * 4) = acc[mt][db] * a;
             }
         }
         __syncthreads();
@@ -627,7 +758,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const float* const buf = reinterpret_cast<const float*>(stage) + mt * (NW * 16 * D);
-            for (int e = tid; e < 16 * (D / 4); e += NT) {
+            for (int e = thread; e < 16 * (D / 4); e += NT) {
                 const int r = e / (D / 4), c4 = e - r * (D / 4);
                 const int lr = mt * 16 + r;
                 floatx4_t o{0.f, 0.f, 0.f, 0.f};
