@@ -405,7 +405,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     __shared__ __attribute__((aligned(1024))) uint16_t stage[NW * 4 * BUF];
     __shared__ float wave_m[NW][MT * 16], wave_l[NW][MT * 16];
     __shared__ int wave_odd[NW];  // whether the wavefront met a tree row's value that is not finite
-    __shared__ uint64_t anc[SV_MAX_DRAFT];
+    __shared__ uint64_t ancs[NW][SV_MAX_DRAFT];  // each wavefront's own copy: it needs no barrier
     __shared__ int64_t scan_tmp[NW];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -459,14 +459,8 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         }
         const uint64_t own_mask = ancestors(up, lane);
         const uint64_t present = __ballot(own_mask != 0);
-        if (wave == 0) anc[lane] = own_mask;  // (read after the barriers below)
-        uint64_t see[MT];  // the draft nodes that this lane's row sees
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int node = min(row0 + mt * 16 + q_of, p.rows - 1) / p.group;
-            const uint64_t m = __shfl(static_cast<unsigned long long>(own_mask), max(node - 1, 0));
-            see[mt] = node == 0 ? 0 : m;
-        }
+        uint64_t* const anc = ancs[wave];
+        anc[lane] = own_mask;
         floatx4_t acc[MT][DB];
         float m[MT], l[MT];
 #pragma unroll
@@ -548,13 +542,15 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         const auto hide = [&](int s, floatx4_t (&sc)[MT][2]) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                uint32_t seen = 0;  // which of the lane's 8 keys its row sees
+                const int node = min(row0 + mt * 16 + q_of, p.rows - 1) / p.group;
+                const uint64_t see = node == 0 ? 0 : anc[node - 1];  // the draft nodes that the lane's row sees
+                uint32_t seen = 0;                                   // which of the lane's 8 keys it does
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     // of the draft node at the lane's first key; -1 is the root, committed keys are below
                     const int j = key_of(s) + kb * 16 + g * 4 - len - 1;
-                    const uint32_t low = j >= 0 ? static_cast<uint32_t>(j < 64 ? see[mt] >> j : 0)
-                                                : static_cast<uint32_t>(see[mt] << min(-j, 4)) | ((1u << min(-j, 4)) - 1);
+                    const uint32_t low = j >= 0 ? static_cast<uint32_t>(j < 64 ? see >> j : 0)
+                                                : static_cast<uint32_t>(see << min(-j, 4)) | ((1u << min(-j, 4)) - 1);
                     seen |= (low & 15u) << (kb * 4);
                 }
 #pragma unroll
@@ -589,7 +585,10 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                 m[mt] = mn;
                 l[mt] *= f;
 #pragma unroll
-                for (int db = 0; db < DB; ++db) acc[mt][db] *= f;
+                for (int db = 0; db < DB; ++db) {
+                    acc[mt][db] *= f;
+                    __builtin_amdgcn_sched_barrier(0);  // one after the other: all at once they fill the vector registers
+                }
             }
         };
         const auto weights = [&](int mt, const floatx4_t (&sc)[MT][2]) {
@@ -697,20 +696,15 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         if (full <= 0) hide(0, sc);
         for (int s = 0; s < mine_n;) {
             raise(sc);
-            bool more;
             do {
-                step(s++, sc, next);
-                if (s >= mine_n || past(next)) {
+                step(s, sc, next);
+                ++s;
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        sc[mt][0] = next[mt][0];
-                        sc[mt][1] = next[mt][1];
-                    }
-                    break;
+                for (int mt = 0; mt < MT; ++mt) {
+                    sc[mt][0] = next[mt][0];
+                    sc[mt][1] = next[mt][1];
                 }
-                step(s++, next, sc);
-                more = s < mine_n && !past(sc);
-            } while (more);
+            } while (s < mine_n && !past(sc));
         }
         __builtin_amdgcn_s_waitcnt(0x0F70);  // no load may land in a buffer that holds sums
         asm volatile("" ::: "memory");
@@ -742,6 +736,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             for (int db = 0; db < DB; ++db) {
                 const int c = (db * 4 + g_at) ^ (q_at & 7);
                 *reinterpret_cast<floatx4_t*>(buf + (wave * 16 + q_at) * D + c * 4) = acc[mt][db] * a;
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         __syncthreads();
