@@ -312,77 +312,88 @@ __device__ __forceinline__ uint64_t ancestors(int up, int lane) {
     return gone ? 0 : mask;
 }
 
-// Key tiles of sequence b (0: absent, a negative length or one that its page
-// table row cannot hold).
-__device__ __forceinline__ int64_t seq_tiles(const AttnPlan& p, int b, int tile_keys) {
-    const int64_t n = p.seq_len[b];
-    const int64_t keys = n + p.k + 1;
+// Key tiles of a sequence of n committed keys (0: absent, a negative length
+// or one that its page table row cannot hold).
+__device__ __forceinline__ int tiles_of(const AttnPlan& p, int n, int tile_keys) {
+    const int64_t keys = static_cast<int64_t>(n) + p.k + 1;
     if (n < 0 || keys > (static_cast<int64_t>(p.max_pages) << p.page_shift)) return 0;
-    return (keys + tile_keys - 1) / tile_keys;
+    return static_cast<int>((keys + tile_keys - 1) / tile_keys);
 }
 
-// Inclusive sum over the workgroup's threads, and the total.
+// Inclusive sum over the workgroup's threads, and the total.  A sequence has
+// at most 2^24 tiles, so a wavefront's sums fit 32 bits.
 template <int NT>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t* tmp) {
+__device__ __forceinline__ int64_t block_scan(int v, int64_t* total, int64_t* tmp) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(static_cast<long long>(v), d);
+        const int o = __shfl_up(v, d);
         if (lane >= d) v += o;
+    }
+    if constexpr (NT == 64) {
+        *total = __builtin_amdgcn_readlane(v, 63);
+        return v;
     }
     __syncthreads();
     if (lane == 63) tmp[wave] = v;
     __syncthreads();
-    int64_t all = 0;
+    int64_t all = 0, mine = v;
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) {
-        if (w < wave) v += tmp[w];
+        if (w < wave) mine += tmp[w];
         all += tmp[w];
     }
     *total = all;
-    return v;
+    return mine;
 }
 
 // What a workgroup finds of the line of all sequences' key tiles, key head
 // by key head: its run, and where the run begins.
 struct Line {
     int64_t begin, end, share;
-    int b;          // the sequence that `begin` lies in
+    int b, len;     // the sequence that `begin` lies in, and its committed keys
     int64_t b_off;  // the line's index of that sequence's first tile
 };
 
 template <int NT>
 __device__ __forceinline__ Line find_run(const AttnPlan& p, int cluster, int tile_keys, int64_t* tmp) {
     __shared__ int64_t found_off;
-    __shared__ int found_b;
-    const int heads = p.kv_heads;
-    const bool once = p.batch <= NT;  // one scan has it all
-    int64_t mine = 0, sum = 0, total;
-    for (int b = threadIdx.x; b < p.batch; b += NT) sum += mine = seq_tiles(p, b, tile_keys);
-    int64_t incl = block_scan<NT>(sum, &total, tmp);
+    __shared__ int found_b, found_len;
+    const int heads = p.kv_heads, tid = threadIdx.x;
     Line r;
+    int64_t total = 0, before_all = 0, incl = 0, all;
+    int n = -1, mine = 0;
+    for (int c = 0; c < p.batch; c += NT) {
+        n = c + tid < p.batch ? p.seq_len[c + tid] : -1;
+        mine = tiles_of(p, n, tile_keys);
+        incl = block_scan<NT>(mine, &all, tmp);
+        total += all;
+    }
+    const bool once = p.batch <= NT;  // the one scan has it all
     total *= heads;
     r.share = (total + p.clusters - 1) / p.clusters;
     if (r.share < 1) r.share = 1;
     r.begin = cluster * r.share;
     r.end = min(r.begin + r.share, total);
     if (r.begin >= r.end) return r;
-    int64_t base = 0;
-    for (int c = 0; base * heads <= r.begin; c += NT) {
-        int64_t all = total;
+    for (int c = 0; c < p.batch; c += NT) {
         if (!once) {
-            mine = c + static_cast<int>(threadIdx.x) < p.batch ? seq_tiles(p, c + threadIdx.x, tile_keys) : 0;
+            n = c + tid < p.batch ? p.seq_len[c + tid] : -1;
+            mine = tiles_of(p, n, tile_keys);
             incl = block_scan<NT>(mine, &all, tmp);
         }
-        const int64_t before = base + incl - mine;
+        const int64_t before = before_all + incl - mine;
         if (mine > 0 && r.begin >= before * heads && r.begin < (before + mine) * heads) {
-            found_b = c + threadIdx.x;
+            found_b = c + tid;
+            found_len = n;
             found_off = before * heads;
         }
-        base += all;
+        before_all += all;
+        if (once || before_all * heads > r.begin) break;
     }
     __syncthreads();
     r.b = found_b;
+    r.len = found_len;
     r.b_off = found_off;
     return r;
 }
@@ -418,20 +429,21 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     const int on_die = blockIdx.x / kAttnDies, per_die = p.clusters / kAttnDies;
     const int cluster = (blockIdx.x % kAttnDies) * per_die + on_die / p.cluster;
     const bool works = on_die < per_die * p.cluster;
-    Line run{0, 0, 1, 0, 0};
+    Line run{0, 0, 1, 0, 0, 0};
     if (works) run = find_run<NT>(p, cluster, TILE, scan_tmp);
 
     for (int ru = on_die % p.cluster; works && ru < p.row_units; ru += p.cluster) {
     int64_t pos = run.begin;
-    int b = run.b;
+    int b = run.b, len = run.len;
     int64_t seq_off = run.b_off;  // the line's index of sequence b's first tile
     AttnSplit split{-1, 0, 0, 0};
-    int nt = pos < run.end ? static_cast<int>(seq_tiles(p, b, TILE)) : 0;
+    int nt = pos < run.end ? tiles_of(p, len, TILE) : 0;
     while (pos < run.end) {
         while (pos >= seq_off + static_cast<int64_t>(nt) * p.kv_heads) {  // the next sequence that has tiles
             seq_off += static_cast<int64_t>(nt) * p.kv_heads;
             ++b;
-            nt = static_cast<int>(seq_tiles(p, b, TILE));
+            len = p.seq_len[b];
+            nt = tiles_of(p, len, TILE);
         }
         const int64_t in_seq = pos - seq_off;
         const int h = static_cast<int>(in_seq / nt);
@@ -441,9 +453,17 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         int row0 = ru * (MT * 16);
         asm volatile("" : "+s"(row0));  // what follows from it is worked out in place: hoisted out of the loop over the
                                         // key heads it would hold registers through the steps
-        const int len = p.seq_len[b];
         const int keys = len + p.k + 1;
+        const int steps = t1 - t0;
+        const auto key_of = [&](int s) { return ((t0 + s) * NW + wave) * STEP; };
         const int32_t* const table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        // Everything that the first steps need is asked for at once; of the
+        // pages, those of the keys themselves, and the root's.
+        const auto page_load = [&](int s) {
+            return table[min(key_of(min(s, steps - 1)) + (lane & 31), keys - 1) >> p.page_shift];
+        };
+        const int pa = page_load(0), pb = page_load(1), pc = page_load(2), pd = page_load(3);
+        const int root_page = table[len >> p.page_shift];
         const int up = parent_of(p, b, lane);
 
         shortx8_t qf[MT][KK];
@@ -471,8 +491,6 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             for (int db = 0; db < DB; ++db) acc[mt][db] = floatx4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        const int steps = t1 - t0;
-        const auto key_of = [&](int s) { return ((t0 + s) * NW + wave) * STEP; };
         // Steps whose keys are all committed ones come first.
         const int full = min(steps, max(0, (len - wave * STEP) / STEP + NW - 1) / NW - t0);
         uint16_t* const mine = stage + wave * (4 * BUF);
@@ -486,16 +504,15 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         // at weight 0): the root's row is read in their place.  Page numbers out
         // of range are read as page 0: the result is then unspecified, the
         // access in bounds.
-        const auto slot_of = [&](int s) {
+        const auto row_at = [&](int page, int pos) {
+            const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
+            return ((id * p.kv_heads + h) << p.page_shift) + (pos & page_mask);
+        };
+        const auto row_of = [&](int s, int page) {
             const int key = key_of(min(s, steps - 1)) + (lane & 31);
             const int j = key - len - 1;
-            if (j < 0) return key;
-            return j < p.k && ((present >> j) & 1) ? key : len;
-        };
-        const auto page_load = [&](int s) { return table[slot_of(s) >> p.page_shift]; };
-        const auto row_of = [&](int s, int page) {
-            const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
-            return ((id * p.kv_heads + h) << p.page_shift) + (slot_of(s) & page_mask);
+            if (j < 0) return row_at(page, key);
+            return j < p.k && ((present >> j) & 1) ? row_at(page, key) : row_at(root_page, len);
         };
         // One operand's rows of a step, straight to LDS.  A load takes whole
         // rows for the head sizes that are powers of two, and where these stand
@@ -645,7 +662,6 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         };
         uint32_t row_v, row_k;  // of steps s + 2 and s + 3
         {
-            const int pa = page_load(0), pb = page_load(1), pc = page_load(2), pd = page_load(3);
             const uint32_t r0 = row_of(0, pa), r1 = row_of(1, pb);
             k_dma(0, r0);
             k_dma(1, r1);
@@ -773,8 +789,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                     for (int j = 0; j <= p.k; ++j) {
                         if (j > 0 && (node == 0 || !((anc[node - 1] >> (j - 1)) & 1))) continue;
                         const int page = table[(len + j) >> p.page_shift];
-                        const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
-                        const uint64_t at = ((id * p.kv_heads + h) << p.page_shift) + ((len + j) & page_mask);
+                        const uint64_t at = row_at(page, len + j);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint16_t x = vc[at * D + c4 * 4 + i];
@@ -798,8 +813,10 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
                 } else {
                     *reinterpret_cast<floatx4_t*>(p.part_acc + (slot * (MT * 16) + lr) * D + c4 * 4) = o;
                     if (c4 == 0) {
-                        p.part_ml[(slot * (MT * 16) + lr) * 2] = mm;
-                        p.part_ml[(slot * (MT * 16) + lr) * 2 + 1] = ll;
+                        // rows of absent nodes are joined as having seen nothing
+                        const bool there = node == 0 || anc[node - 1] != 0;
+                        *reinterpret_cast<float2*>(p.part_ml + (slot * (MT * 16) + lr) * 2) =
+                            there ? float2{mm, ll} : float2{-__builtin_inff(), 0.f};
                     }
                 }
             }
@@ -811,7 +828,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     }
     // Absent sequences have no tiles; their rows are zeros.
     for (int b = blockIdx.x; b < p.batch; b += kAttnWgs) {
-        if (seq_tiles(p, b, TILE) > 0) continue;
+        if (tiles_of(p, p.seq_len[b], TILE) > 0) continue;
         const int64_t n = static_cast<int64_t>(p.k + 1) * p.q_heads;
         for (int64_t e = tid; e < n * (D / 8); e += NT)
             reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + b * n * D)[e] = uint4{0, 0, 0, 0};
@@ -827,55 +844,63 @@ __global__ __launch_bounds__(256) void k_tree_combine(AttnPlan p) {
     const int cluster = blockIdx.x / p.row_units, ru = blockIdx.x - cluster * p.row_units;
     const AttnSplit s = p.splits[blockIdx.x];
     if (s.b < 0) return;
-    constexpr int LANES = D / 4, GROUPS = 64 / LANES;
+    constexpr int LANES = D / 4, GROUPS = 64 / LANES, AHEAD = 4;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int unit_rows = p.row_tiles * 16;
     const int lr = blockIdx.y * 4 + wave;
     const int row = ru * unit_rows + lr;
     if (row >= p.rows) return;
-    const int node = row / p.group, head = s.head * p.group + row - node * p.group;
-    const int64_t at = (static_cast<int64_t>(s.b) * (p.k + 1) + node) * p.q_heads + head;
-    const uint64_t mask = ancestors(parent_of(p, s.b, lane), lane);
-    const uint64_t there_mask = __ballot(mask != 0);
-    const bool there = node == 0 || ((there_mask >> (node - 1)) & 1);
     const int count = s.last - cluster + 1;
-    const auto slot_row = [&](int i) {
-        const int64_t slot = (static_cast<int64_t>(cluster + i) * p.row_units + ru) * 2 + (i == 0 ? s.slot1 : 0);
-        return slot * unit_rows + lr;
-    };
-    float mm = -__builtin_inff();
-    for (int i = lane; i < count; i += 64) mm = fmaxf(mm, p.part_ml[slot_row(i) * 2]);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
-    const int group = lane / LANES, c = (lane - group * LANES) * 4;
-    float ll = 0.f;
+    const int group = min(lane / LANES, GROUPS - 1), c = (lane % LANES) * 4;
+    float m = -__builtin_inff(), l = 0.f;
     floatx4_t o{0.f, 0.f, 0.f, 0.f};
-    if (group < GROUPS) {
-#pragma unroll 4
-        for (int i = group; i < count; i += GROUPS) {
-            const int64_t r = slot_row(i);
-            const float mw = p.part_ml[r * 2], lw = p.part_ml[r * 2 + 1];
-            const float a = mw == -__builtin_inff() ? 0.f : (mw == mm ? 1.f : exp2_fast(mw - mm));
-            ll += lw * a;
-            o += *reinterpret_cast<const floatx4_t*>(p.part_acc + r * D + c) * a;
+    for (int base = group; base < count; base += GROUPS * AHEAD) {
+        float2 ml[AHEAD];
+        floatx4_t x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int part = min(base + i * GROUPS, count - 1);
+            const int64_t slot = (static_cast<int64_t>(cluster + part) * p.row_units + ru) * 2 + (part == 0 ? s.slot1 : 0);
+            ml[i] = reinterpret_cast<const float2*>(p.part_ml)[slot * unit_rows + lr];
+            x[i] = *reinterpret_cast<const floatx4_t*>(p.part_acc + (slot * unit_rows + lr) * D + c);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (base + i * GROUPS >= count || ml[i].x == -__builtin_inff()) continue;
+            const float mn = fmaxf(m, ml[i].x);
+            const float a = m == mn ? 1.f : exp2_fast(m - mn), b = ml[i].x == mn ? 1.f : exp2_fast(ml[i].x - mn);
+            m = mn;
+            l = l * a + ml[i].y * b;
+            o = o * a + x[i] * b;
         }
     }
-    const float l0 = ll;
+    // The groups' results, in their order.
+    const float m0 = m, l0 = l;
     const floatx4_t o0 = o;
 #pragma unroll
-    for (int q = 1; q < GROUPS; ++q) {  // the groups' sums, in order
+    for (int q = 1; q < GROUPS; ++q) {
         const int from = (lane + q * LANES) & 63;
-        ll += __shfl(l0, from);
+        const float mq = __shfl(m0, from), lq = __shfl(l0, from);
+        floatx4_t oq;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += __shfl(o0[i], from);
+        for (int i = 0; i < 4; ++i) oq[i] = __shfl(o0[i], from);
+        if (mq == -__builtin_inff()) continue;
+        const float mn = fmaxf(m, mq);
+        const float a = m == mn ? 1.f : exp2_fast(m - mn), b = mq == mn ? 1.f : exp2_fast(mq - mn);
+        m = mn;
+        l = l * a + lq * b;
+        o = o * a + oq * b;
     }
     if (lane >= LANES) return;
-    const float inv = 1.f / ll;
+    const bool there = m != -__builtin_inff();
+    const int node = row / p.group, head = s.head * p.group + row - node * p.group;
+    const int64_t at = (static_cast<int64_t>(s.b) * (p.k + 1) + node) * p.q_heads + head;
+    const float inv = 1.f / l;
     shortx4_t x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = there ? to16<F16>(o[i] * inv) : short{0};
     *reinterpret_cast<shortx4_t*>(static_cast<uint16_t*>(p.out) + at * D + c) = x;
-    if (p.lse && lane == 0) p.lse[at] = there ? (mm + __log2f(ll)) * 0.69314718055994531f : -__builtin_inff();
+    if (p.lse && lane == 0) p.lse[at] = there ? (m + __log2f(l)) * 0.69314718055994531f : -__builtin_inff();
 }
 
 template <bool F16, int D>
