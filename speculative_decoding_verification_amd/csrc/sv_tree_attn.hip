@@ -136,141 +136,146 @@ struct VAddress {
 // All of a step's reads in one piece of assembly that waits for them: the
 // compiler cannot tell a transposing read from the loads in flight to the other
 // buffers and would wait for all of these too.  a[kb][kk]: K, 16 keys kb; lo,
-// hi[db]: V, the first and second 16 keys.
+// hi[db]: V, the first and second 16 keys; page: the lane's page number.
 template <int D>
 __device__ __forceinline__ void read_step(const KAddress<D>& k, const VAddress<D>& v, shortx8_t (&a)[2][D / 32],
-                                          shortx4_t (&lo)[D / 16], shortx4_t (&hi)[D / 16]) {
+                                          shortx4_t (&lo)[D / 16], shortx4_t (&hi)[D / 16],
+                                          uint32_t page_at, int& page) {
     if constexpr (D == 64)
         asm volatile(
-                     "ds_read_b128 %0, %12 offset:0\n\t"
-                     "ds_read_b128 %1, %13 offset:0\n\t"
-                     "ds_read_b128 %2, %12 offset:2048\n\t"
-                     "ds_read_b128 %3, %13 offset:2048\n\t"
-                     "ds_read_b64_tr_b16 %4, %14 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %5, %14 offset:2048\n\t"
-                     "ds_read_b64_tr_b16 %6, %15 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %7, %15 offset:2048\n\t"
-                     "ds_read_b64_tr_b16 %8, %16 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %9, %16 offset:2048\n\t"
-                     "ds_read_b64_tr_b16 %10, %17 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %11, %17 offset:2048\n\t"
+                     "ds_read_b128 %0, %13 offset:0\n\t"
+                     "ds_read_b128 %1, %14 offset:0\n\t"
+                     "ds_read_b128 %2, %13 offset:2048\n\t"
+                     "ds_read_b128 %3, %14 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %4, %15 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %5, %15 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %6, %16 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %7, %16 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %8, %17 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %9, %17 offset:2048\n\t"
+                     "ds_read_b64_tr_b16 %10, %18 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %11, %18 offset:2048\n\t"
+                     "ds_read_b32 %12, %19\n\t"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[1][0]), "=&a"(a[1][1]), "=&v"(lo[0]), "=&v"(hi[0]),
-                       "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3])
-                     : "v"(k.at(0)), "v"(k.at(1)), "v"(v.at(0)), "v"(v.at(1)), "v"(v.at(2)), "v"(v.at(3))
+                       "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(page)
+                     : "v"(k.at(0)), "v"(k.at(1)), "v"(v.at(0)), "v"(v.at(1)), "v"(v.at(2)), "v"(v.at(3)), "v"(page_at)
                      : "memory");
     else if constexpr (D == 96)
         asm volatile(
-                     "ds_read_b128 %0, %18 offset:0\n\t"
-                     "ds_read_b128 %1, %18 offset:64\n\t"
-                     "ds_read_b128 %2, %18 offset:128\n\t"
-                     "ds_read_b128 %3, %18 offset:3072\n\t"
-                     "ds_read_b128 %4, %18 offset:3136\n\t"
-                     "ds_read_b128 %5, %18 offset:3200\n\t"
-                     "ds_read_b64_tr_b16 %6, %19 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %7, %19 offset:3072\n\t"
-                     "ds_read_b64_tr_b16 %8, %20 offset:32\n\t"
-                     "ds_read_b64_tr_b16 %9, %20 offset:3104\n\t"
-                     "ds_read_b64_tr_b16 %10, %19 offset:64\n\t"
-                     "ds_read_b64_tr_b16 %11, %19 offset:3136\n\t"
-                     "ds_read_b64_tr_b16 %12, %20 offset:96\n\t"
-                     "ds_read_b64_tr_b16 %13, %20 offset:3168\n\t"
-                     "ds_read_b64_tr_b16 %14, %19 offset:128\n\t"
-                     "ds_read_b64_tr_b16 %15, %19 offset:3200\n\t"
-                     "ds_read_b64_tr_b16 %16, %20 offset:160\n\t"
-                     "ds_read_b64_tr_b16 %17, %20 offset:3232\n\t"
+                     "ds_read_b128 %0, %19 offset:0\n\t"
+                     "ds_read_b128 %1, %19 offset:64\n\t"
+                     "ds_read_b128 %2, %19 offset:128\n\t"
+                     "ds_read_b128 %3, %19 offset:3072\n\t"
+                     "ds_read_b128 %4, %19 offset:3136\n\t"
+                     "ds_read_b128 %5, %19 offset:3200\n\t"
+                     "ds_read_b64_tr_b16 %6, %20 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %7, %20 offset:3072\n\t"
+                     "ds_read_b64_tr_b16 %8, %21 offset:32\n\t"
+                     "ds_read_b64_tr_b16 %9, %21 offset:3104\n\t"
+                     "ds_read_b64_tr_b16 %10, %20 offset:64\n\t"
+                     "ds_read_b64_tr_b16 %11, %20 offset:3136\n\t"
+                     "ds_read_b64_tr_b16 %12, %21 offset:96\n\t"
+                     "ds_read_b64_tr_b16 %13, %21 offset:3168\n\t"
+                     "ds_read_b64_tr_b16 %14, %20 offset:128\n\t"
+                     "ds_read_b64_tr_b16 %15, %20 offset:3200\n\t"
+                     "ds_read_b64_tr_b16 %16, %21 offset:160\n\t"
+                     "ds_read_b64_tr_b16 %17, %21 offset:3232\n\t"
+                     "ds_read_b32 %18, %22\n\t"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[0][2]), "=&a"(a[1][0]), "=&a"(a[1][1]),
                        "=&a"(a[1][2]), "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]),
                        "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]),
-                       "=&v"(hi[5])
-                     : "v"(k.base), "v"(v.base + v.odd), "v"(v.base - v.odd)
+                       "=&v"(hi[5]), "=&v"(page)
+                     : "v"(k.base), "v"(v.base + v.odd), "v"(v.base - v.odd), "v"(page_at)
                      : "memory");
     else if constexpr (D == 128)
         asm volatile(
-                     "ds_read_b128 %0, %24 offset:0\n\t"
-                     "ds_read_b128 %1, %25 offset:0\n\t"
-                     "ds_read_b128 %2, %26 offset:0\n\t"
-                     "ds_read_b128 %3, %27 offset:0\n\t"
-                     "ds_read_b128 %4, %24 offset:4096\n\t"
-                     "ds_read_b128 %5, %25 offset:4096\n\t"
-                     "ds_read_b128 %6, %26 offset:4096\n\t"
-                     "ds_read_b128 %7, %27 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %8, %28 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %9, %28 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %10, %29 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %11, %29 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %12, %30 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %13, %30 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %14, %31 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %15, %31 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %16, %32 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %17, %32 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %18, %33 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %19, %33 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %20, %34 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %21, %34 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %22, %35 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %23, %35 offset:4096\n\t"
+                     "ds_read_b128 %0, %25 offset:0\n\t"
+                     "ds_read_b128 %1, %26 offset:0\n\t"
+                     "ds_read_b128 %2, %27 offset:0\n\t"
+                     "ds_read_b128 %3, %28 offset:0\n\t"
+                     "ds_read_b128 %4, %25 offset:4096\n\t"
+                     "ds_read_b128 %5, %26 offset:4096\n\t"
+                     "ds_read_b128 %6, %27 offset:4096\n\t"
+                     "ds_read_b128 %7, %28 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %8, %29 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %9, %29 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %10, %30 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %11, %30 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %12, %31 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %13, %31 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %14, %32 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %15, %32 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %16, %33 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %17, %33 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %18, %34 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %19, %34 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %20, %35 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %21, %35 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %22, %36 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %23, %36 offset:4096\n\t"
+                     "ds_read_b32 %24, %37\n\t"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[0][2]), "=&a"(a[0][3]), "=&a"(a[1][0]),
                        "=&a"(a[1][1]), "=&a"(a[1][2]), "=&a"(a[1][3]), "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]),
                        "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]),
                        "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]), "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]),
-                       "=&v"(hi[7])
+                       "=&v"(hi[7]), "=&v"(page)
                      : "v"(k.at(0)), "v"(k.at(1)), "v"(k.at(2)), "v"(k.at(3)), "v"(v.at(0)), "v"(v.at(1)),
-                       "v"(v.at(2)), "v"(v.at(3)), "v"(v.at(4)), "v"(v.at(5)), "v"(v.at(6)), "v"(v.at(7))
+                       "v"(v.at(2)), "v"(v.at(3)), "v"(v.at(4)), "v"(v.at(5)), "v"(v.at(6)), "v"(v.at(7)), "v"(page_at)
                      : "memory");
     else
         asm volatile(
-                     "ds_read_b128 %0, %48 offset:0\n\t"
-                     "ds_read_b128 %1, %49 offset:0\n\t"
-                     "ds_read_b128 %2, %50 offset:0\n\t"
-                     "ds_read_b128 %3, %51 offset:0\n\t"
-                     "ds_read_b128 %4, %52 offset:0\n\t"
-                     "ds_read_b128 %5, %53 offset:0\n\t"
-                     "ds_read_b128 %6, %54 offset:0\n\t"
-                     "ds_read_b128 %7, %55 offset:0\n\t"
-                     "ds_read_b128 %8, %48 offset:8192\n\t"
-                     "ds_read_b128 %9, %49 offset:8192\n\t"
-                     "ds_read_b128 %10, %50 offset:8192\n\t"
-                     "ds_read_b128 %11, %51 offset:8192\n\t"
-                     "ds_read_b128 %12, %52 offset:8192\n\t"
-                     "ds_read_b128 %13, %53 offset:8192\n\t"
-                     "ds_read_b128 %14, %54 offset:8192\n\t"
-                     "ds_read_b128 %15, %55 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %16, %56 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %17, %56 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %18, %57 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %19, %57 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %20, %58 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %21, %58 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %22, %59 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %23, %59 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %24, %60 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %25, %60 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %26, %61 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %27, %61 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %28, %62 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %29, %62 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %30, %63 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %31, %63 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %32, %64 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %33, %64 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %34, %65 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %35, %65 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %36, %66 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %37, %66 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %38, %67 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %39, %67 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %40, %68 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %41, %68 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %42, %69 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %43, %69 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %44, %70 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %45, %70 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %46, %71 offset:0\n\t"
-                     "ds_read_b64_tr_b16 %47, %71 offset:8192\n\t"
+                     "ds_read_b128 %0, %49 offset:0\n\t"
+                     "ds_read_b128 %1, %50 offset:0\n\t"
+                     "ds_read_b128 %2, %51 offset:0\n\t"
+                     "ds_read_b128 %3, %52 offset:0\n\t"
+                     "ds_read_b128 %4, %53 offset:0\n\t"
+                     "ds_read_b128 %5, %54 offset:0\n\t"
+                     "ds_read_b128 %6, %55 offset:0\n\t"
+                     "ds_read_b128 %7, %56 offset:0\n\t"
+                     "ds_read_b128 %8, %49 offset:8192\n\t"
+                     "ds_read_b128 %9, %50 offset:8192\n\t"
+                     "ds_read_b128 %10, %51 offset:8192\n\t"
+                     "ds_read_b128 %11, %52 offset:8192\n\t"
+                     "ds_read_b128 %12, %53 offset:8192\n\t"
+                     "ds_read_b128 %13, %54 offset:8192\n\t"
+                     "ds_read_b128 %14, %55 offset:8192\n\t"
+                     "ds_read_b128 %15, %56 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %16, %57 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %17, %57 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %18, %58 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %19, %58 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %20, %59 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %21, %59 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %22, %60 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %23, %60 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %24, %61 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %25, %61 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %26, %62 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %27, %62 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %28, %63 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %29, %63 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %30, %64 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %31, %64 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %32, %65 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %33, %65 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %34, %66 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %35, %66 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %36, %67 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %37, %67 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %38, %68 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %39, %68 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %40, %69 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %41, %69 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %42, %70 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %43, %70 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %44, %71 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %45, %71 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %46, %72 offset:0\n\t"
+                     "ds_read_b64_tr_b16 %47, %72 offset:8192\n\t"
+                     "ds_read_b32 %48, %73\n\t"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&a"(a[0][0]), "=&a"(a[0][1]), "=&a"(a[0][2]), "=&a"(a[0][3]), "=&a"(a[0][4]),
                        "=&a"(a[0][5]), "=&a"(a[0][6]), "=&a"(a[0][7]), "=&a"(a[1][0]), "=&a"(a[1][1]),
@@ -280,11 +285,11 @@ __device__ __forceinline__ void read_step(const KAddress<D>& k, const VAddress<D
                        "=&v"(hi[5]), "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]), "=&v"(hi[7]), "=&v"(lo[8]),
                        "=&v"(hi[8]), "=&v"(lo[9]), "=&v"(hi[9]), "=&v"(lo[10]), "=&v"(hi[10]), "=&v"(lo[11]),
                        "=&v"(hi[11]), "=&v"(lo[12]), "=&v"(hi[12]), "=&v"(lo[13]), "=&v"(hi[13]), "=&v"(lo[14]),
-                       "=&v"(hi[14]), "=&v"(lo[15]), "=&v"(hi[15])
+                       "=&v"(hi[14]), "=&v"(lo[15]), "=&v"(hi[15]), "=&v"(page)
                      : "v"(k.at(0)), "v"(k.at(1)), "v"(k.at(2)), "v"(k.at(3)), "v"(k.at(4)), "v"(k.at(5)),
                        "v"(k.at(6)), "v"(k.at(7)), "v"(v.at(0)), "v"(v.at(1)), "v"(v.at(2)), "v"(v.at(3)),
                        "v"(v.at(4)), "v"(v.at(5)), "v"(v.at(6)), "v"(v.at(7)), "v"(v.at(8)), "v"(v.at(9)),
-                       "v"(v.at(10)), "v"(v.at(11)), "v"(v.at(12)), "v"(v.at(13)), "v"(v.at(14)), "v"(v.at(15))
+                       "v"(v.at(10)), "v"(v.at(11)), "v"(v.at(12)), "v"(v.at(13)), "v"(v.at(14)), "v"(v.at(15)), "v"(page_at)
                      : "memory");
 }
 
@@ -417,6 +422,7 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     __shared__ float wave_m[NW][MT * 16], wave_l[NW][MT * 16];
     __shared__ int wave_odd[NW];  // whether the wavefront met a tree row's value that is not finite
     __shared__ uint64_t ancs[NW][SV_MAX_DRAFT];  // each wavefront's own copy: it needs no barrier
+    __shared__ int32_t pages[NW][2][64];  // page numbers of steps to come, by parity
     __shared__ int64_t scan_tmp[NW];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -459,10 +465,10 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         const int32_t* const table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
         // Everything that the first steps need is asked for at once; of the
         // pages, those of the keys themselves, and the root's.
-        const auto page_load = [&](int s) {
-            return table[min(key_of(min(s, steps - 1)) + (lane & 31), keys - 1) >> p.page_shift];
+        const auto page_of = [&](int s) {
+            return table + (min(key_of(min(s, steps - 1)) + (lane & 31), keys - 1) >> p.page_shift);
         };
-        const int pa = page_load(0), pb = page_load(1), pc = page_load(2), pd = page_load(3);
+        const int pa = *page_of(0), pb = *page_of(1), pc = *page_of(2), pd = *page_of(3);
         const int root_page = table[len >> p.page_shift];
         const int up = parent_of(p, b, lane);
 
@@ -477,10 +483,14 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             for (int kk = 0; kk < KK; ++kk)
                 qf[mt][kk] = *reinterpret_cast<const shortx8_t*>(src + (kk * 4 + g) * 8);
         }
-        const uint64_t own_mask = ancestors(up, lane);
+        const uint64_t own_mask = p.k > 0 ? ancestors(up, lane) : 0;
         const uint64_t present = __ballot(own_mask != 0);
         uint64_t* const anc = ancs[wave];
         anc[lane] = own_mask;
+        // Queries and page numbers are here: without this wait the compiler
+        // would wait for the queries inside the loop, and so for all loads.
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+
         floatx4_t acc[MT][DB];
         float m[MT], l[MT];
 #pragma unroll
@@ -493,6 +503,8 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
 
         // Steps whose keys are all committed ones come first.
         const int full = min(steps, max(0, (len - wave * STEP) / STEP + NW - 1) / NW - t0);
+        // Steps that hold any key for this wavefront.
+        const int mine_n = min(steps, max(0, (keys - wave * STEP + STEP - 1) / STEP + NW - 1) / NW - t0);
         uint16_t* const mine = stage + wave * (4 * BUF);
         const uint32_t lds = static_cast<uint32_t>(
             reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t*)mine));
@@ -508,11 +520,14 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             const uint32_t id = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages) ? page : 0;
             return ((id * p.kv_heads + h) << p.page_shift) + (pos & page_mask);
         };
+        const uint32_t root_row = row_at(root_page, len);
         const auto row_of = [&](int s, int page) {
             const int key = key_of(min(s, steps - 1)) + (lane & 31);
+            const uint32_t row = row_at(page, key);
+            if (s < full) return row;
             const int j = key - len - 1;
-            if (j < 0) return row_at(page, key);
-            return j < p.k && ((present >> j) & 1) ? row_at(page, key) : row_at(root_page, len);
+            const bool there = j < 0 || (j < p.k && ((present >> (j & 63)) & 1));
+            return there ? row : root_row;
         };
         // One operand's rows of a step, straight to LDS.  A load takes whole
         // rows for the head sizes that are powers of two, and where these stand
@@ -627,23 +642,40 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         // here and added where the sums are written.
         bool odd = false;
         const auto clear_odd = [&](int s) {
-            uint16_t* const vs = mine + (2 + (s & 1)) * BUF;
-#pragma unroll 1
-            for (int e = lane; e < BUF; e += 64)
-                if (nonfinite16<F16>(vs[e])) {
-                    vs[e] = 0;
-                    odd = true;
+            uint4* const vs = reinterpret_cast<uint4*>(mine + (2 + (s & 1)) * BUF);
+            constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u;
+            bool here = false;
+#pragma unroll
+            for (int i = 0; i < BUF / 512; ++i) {
+                const uint4 x = vs[i * 64 + lane];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // a half of y is 0 where that value's exponent is all ones
+                    const uint32_t y = (w[j] & e) ^ e;
+                    here = here || (((y - 0x00010001u) & ~y & 0x80008000u) != 0);
                 }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+            if (__any(here)) {
+                uint16_t* const v = mine + (2 + (s & 1)) * BUF;
+#pragma unroll 1
+                for (int r = max(0, len - key_of(s)); r < STEP; ++r)  // the tree's rows only: every row sees the others
+#pragma unroll 1
+                    for (int d = lane; d < D; d += 64)
+                        if (nonfinite16<F16>(v[r * D + d])) {
+                            v[r * D + d] = 0;
+                            odd = true;
+                        }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
         };
 
         // While step s is worked on, the scores of step s + 1 are formed (its K
         // has landed), and K of steps s + 2 and s + 3 and V of steps s + 1 and
         // s + 2 are on their way: a buffer is filled again as soon as it has
-        // been read.  Page numbers are asked for one step ahead of the rows.
-        // Past the last step the loads repeat its rows, so that the count of
-        // loads in flight is the same at every wait.
-        constexpr int kTwo = 2 * NL;
+        // been read.  Page numbers are asked for a step ahead of the rows.
+        // Nothing is loaded past the last step, so the last two steps wait for
+        // fewer loads in flight.
+        constexpr int kOne = NL, kTwo = 2 * NL;
         const auto landed = [&](auto left) {  // all but the last `left` loads
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0x0F70 | (decltype(left)::value & 15) | ((decltype(left)::value >> 4) << 14));
@@ -653,37 +685,50 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
         floatx4_t sc[MT][2], next[MT][2];
         shortx8_t a[2][KK];
         shortx4_t lo[DB], hi[DB];
-        const auto read = [&](int s) {  // K of step s, V of step s - 1
+        // Page numbers go through LDS too: for one loaded to a register the
+        // compiler would wait for every load in flight.
+        const auto page_dma = [&](int s) {
+            __builtin_amdgcn_global_load_lds((const void*)page_of(s),
+                (__attribute__((address_space(3))) void*)&pages[wave][s & 1][0], 4, 0, 0);
+        };
+        const uint32_t pages_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+            (__attribute__((address_space(3))) int32_t*)&pages[wave][0][lane]));
+        int page;
+        const auto read = [&](int s) {  // K of step s, V of step s - 1, the pages of step s + 3
             KAddress<D> k = k_at;
             VAddress<D> v = v_at;
             k.base += (s & 1) * (BUF * 2);
             v.base += (~s & 1) * (BUF * 2);
-            read_step<D>(k, v, a, lo, hi);
+            read_step<D>(k, v, a, lo, hi, pages_at + (~s & 1) * 256, page);
         };
         uint32_t row_v, row_k;  // of steps s + 2 and s + 3
         {
             const uint32_t r0 = row_of(0, pa), r1 = row_of(1, pb);
-            k_dma(0, r0);
-            k_dma(1, r1);
-            v_dma(0, r0);
-            landed(std::integral_constant<int, kTwo>{});
-            read(0);  // (nothing of V yet)
-            scores(a, sc);
             row_v = row_of(2, pc);
-            k_dma(2, row_v);
-            v_dma(1, r1);
             row_k = row_of(3, pd);
+            if (mine_n > 0) {
+                page_dma(4);
+                k_dma(0, r0);
+                if (mine_n > 1) k_dma(1, r1);
+                v_dma(0, r0);
+                if (mine_n > 1) landed(std::integral_constant<int, kTwo>{});
+                else landed(std::integral_constant<int, kOne>{});
+                read(0);  // (nothing of V yet)
+                scores(a, sc);
+                if (mine_n > 2) k_dma(2, row_v);
+                if (mine_n > 1) v_dma(1, r1);
+            }
         }
-        // Steps that hold any key for this wavefront.
-        const int mine_n = min(steps, max(0, (keys - wave * STEP + STEP - 1) / STEP + NW - 1) / NW - t0);
-        const auto step = [&](int s, floatx4_t (&sc)[MT][2], floatx4_t (&next)[MT][2]) {
-            landed(std::integral_constant<int, kTwo>{});
-            const bool tail = s >= full;
-            if (tail) clear_odd(s);
+        const auto step = [&](auto hot, int s) {
+            constexpr bool HOT = decltype(hot)::value;
+            if (HOT || s + 2 < mine_n) landed(std::integral_constant<int, kTwo>{});
+            else if (s + 2 == mine_n) landed(std::integral_constant<int, kOne>{});
+            else landed(std::integral_constant<int, 0>{});
+            if (!HOT && s >= full) clear_odd(s);
             read(s + 1);
-            const int page = page_load(s + 4);
-            k_dma(s + 3, row_k);
-            v_dma(s + 2, row_v);
+            page_dma(s + 5);
+            if (HOT || s + 3 < mine_n) k_dma(s + 3, row_k);
+            if (HOT || s + 2 < mine_n) v_dma(s + 2, row_v);
             __builtin_amdgcn_sched_barrier(0);
             // One block without branches or memory: the next step's scores and
             // this one's products on the matrix cores, its weights beside them.
@@ -707,20 +752,31 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             __builtin_amdgcn_sched_barrier(0);
             row_v = row_k;
             row_k = row_of(s + 4, page);
-            if (s + 1 >= full) hide(s + 1, next);
+            if (!HOT && s + 1 >= full) hide(s + 1, next);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                sc[mt][0] = next[mt][0];
+                sc[mt][1] = next[mt][1];
+            }
         };
-        if (full <= 0) hide(0, sc);
+        if (full <= 0 && mine_n > 0) hide(0, sc);
+        // Steps that are followed by three more and have only committed keys,
+        // the next one's too, need none of the conditions (and with a load that
+        // may not be there the compiler would wait for all of them at each
+        // page number).
+        const int hot_n = min(mine_n - 3, full - 1);
         for (int s = 0; s < mine_n;) {
             raise(sc);
-            do {
-                step(s, sc, next);
-                ++s;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    sc[mt][0] = next[mt][0];
-                    sc[mt][1] = next[mt][1];
-                }
-            } while (s < mine_n && !past(sc));
+            bool again = false;
+            while (s < hot_n) {
+                step(std::true_type{}, s++);
+                if ((again = past(sc))) break;
+            }
+            if (again) continue;
+            while (s < mine_n) {
+                step(std::false_type{}, s++);
+                if (s < mine_n && past(sc)) break;
+            }
         }
         __builtin_amdgcn_s_waitcnt(0x0F70);  // no load may land in a buffer that holds sums
         asm volatile("" ::: "memory");

@@ -177,6 +177,17 @@ def test_attention_value_nan_reaches_only_rows_that_see_it(dev):
             assert torch.equal(got[:, r], want[:, r])
 
 
+@pytest.mark.parametrize("pos", [0, 63, 69])
+def test_attention_value_nan_of_a_committed_key_reaches_every_row(dev, pos):
+    c = Case(dev, k=9, hq=8, hkv=2, lens=(70,), fill=0.0)
+    want, _ = run_attention(c)
+    c.vc[c.table[0, pos // 16], 1, pos % 16, 9] = float("nan")
+    got, _ = run_attention(c)
+    assert torch.isnan(got[0, :, 4:, 9]).all()
+    keep = [d for d in range(128) if d != 9]
+    assert torch.equal(got[..., keep], want[..., keep]) and torch.equal(got[:, :, :4], want[:, :, :4])
+
+
 def test_attention_is_reproducible_and_leaves_inputs(dev):
     c = Case(dev, k=16, hq=16, hkv=2, lens=(900, 33, 2000), fill=0.0)
     a = c.args()
