@@ -420,6 +420,8 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
     constexpr int BUF = STEP * D;  // elements of one buffer
     __shared__ __attribute__((aligned(1024))) uint16_t stage[NW * 4 * BUF];
     __shared__ float wave_m[NW][MT * 16], wave_l[NW][MT * 16];
+    __shared__ float row_f[MT * 16];      // what a row's sum is multiplied by as it is written
+    __shared__ int64_t row_to[MT * 16];   // where: row of the output, or of the partial results; -1 nowhere
     __shared__ int wave_odd[NW];  // whether the wavefront met a tree row's value that is not finite
     __shared__ uint64_t ancs[NW][SV_MAX_DRAFT];  // each wavefront's own copy: it needs no barrier
     __shared__ int32_t pages[NW][2][64];  // page numbers of steps to come, by parity
@@ -797,84 +799,89 @@ __global__ __launch_bounds__(attn_waves(D) * 64, 1) void k_tree_attn(AttnPlan p)
             }
         }
         __syncthreads();  // and every wavefront has left the buffers
+        const bool whole = t0 == 0 && t1 == nt;
+        // A cluster's first slot takes the keys that its run begins with, its
+        // second those that go on in the next run.
+        const int second = pos != run.begin;
+        if (t0 == 0 && !whole)
+            split = AttnSplit{b, h, static_cast<int>((unit_off + nt - 1) / run.share), second};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float mm = wave_m[0][mt * 16 + q_at];
 #pragma unroll
             for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][mt * 16 + q_at]);
-            const float a = m[mt] == -__builtin_inff() ? 0.f : (m[mt] == mm ? 1.f : exp2_fast(m[mt] - mm));
+            const float f = m[mt] == -__builtin_inff() ? 0.f : (m[mt] == mm ? 1.f : exp2_fast(m[mt] - mm));
             float* const buf = reinterpret_cast<float*>(stage) + mt * (NW * 16 * D);
 #pragma unroll
             for (int db = 0; db < DB; ++db) {
                 const int c = (db * 4 + g_at) ^ (q_at & 7);
-                *reinterpret_cast<floatx4_t*>(buf + (wave * 16 + q_at) * D + c * 4) = acc[mt][db] * a;
+                *reinterpret_cast<floatx4_t*>(buf + (wave * 16 + q_at) * D + c * 4) = acc[mt][db] * f;
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if (thread < MT * 16) {  // a thread settles a row
+            const int row = row0 + thread;
+            float mm = wave_m[0][thread], ll = 0.f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][thread]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float mw = wave_m[w][thread];
+                ll += mw == -__builtin_inff() ? 0.f : wave_l[w][thread] * (mw == mm ? 1.f : exp2_fast(mw - mm));
+            }
+            const int node = min(row, p.rows - 1) / p.group;
+            const bool there = row < p.rows && (node == 0 || anc[node - 1] != 0);
+            if (whole) {
+                const int head = h * p.group + row - node * p.group;
+                const int64_t at = (static_cast<int64_t>(b) * (p.k + 1) + node) * p.q_heads + head;
+                row_to[thread] = row < p.rows ? at : -1;
+                row_f[thread] = there ? 1.f / ll : 0.f;
+                if (p.lse && row < p.rows)
+                    p.lse[at] = there ? (mm + __log2f(ll)) * 0.69314718055994531f : -__builtin_inff();
+            } else {
+                // rows of absent nodes are joined as having seen nothing
+                const int64_t at =
+                    ((static_cast<int64_t>(cluster) * p.row_units + ru) * 2 + second) * (MT * 16) + thread;
+                row_to[thread] = row < p.rows ? at : -1;
+                row_f[thread] = 1.f;
+                reinterpret_cast<float2*>(p.part_ml)[at] = there ? float2{mm, ll} : float2{-__builtin_inff(), 0.f};
+            }
+        }
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == nt;
         int any_odd = 0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) any_odd |= wave_odd[w];
-        // A cluster's first slot takes the keys that its run begins with, its
-        // second those that go on in the next run.
-        const int second = pos != run.begin;
-        const int64_t slot = (static_cast<int64_t>(cluster) * p.row_units + ru) * 2 + second;
-        if (t0 == 0 && !whole)
-            split = AttnSplit{b, h, static_cast<int>((unit_off + nt - 1) / run.share), second};
+#pragma unroll 4
+        for (int e = thread; e < MT * 16 * (D / 4); e += NT) {
+            const int lr = e / (D / 4), c4 = e % (D / 4);
+            const int64_t to = row_to[lr];
+            const float f = row_f[lr];
+            const float* const buf = reinterpret_cast<const float*>(stage) + (lr >> 4) * (NW * 16 * D);
+            floatx4_t o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const float* const buf = reinterpret_cast<const float*>(stage) + mt * (NW * 16 * D);
-            for (int e = thread; e < 16 * (D / 4); e += NT) {
-                const int r = e / (D / 4), c4 = e - r * (D / 4);
-                const int lr = mt * 16 + r;
-                floatx4_t o{0.f, 0.f, 0.f, 0.f};
-                float mm = wave_m[0][lr], ll = 0.f;
-#pragma unroll
-                for (int w = 1; w < NW; ++w) mm = fmaxf(mm, wave_m[w][lr]);
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    o += *reinterpret_cast<const floatx4_t*>(buf + (w * 16 + r) * D + ((c4 ^ (r & 7)) << 2));
-                    const float mw = wave_m[w][lr];
-                    ll += mw == -__builtin_inff() ? 0.f : wave_l[w][lr] * (mw == mm ? 1.f : exp2_fast(mw - mm));
-                }
-                const int row = row0 + lr;
-                const int node = min(row, p.rows - 1) / p.group;
-                if (any_odd) {
+            for (int w = 0; w < NW; ++w)
+                o += *reinterpret_cast<const floatx4_t*>(buf + (w * 16 + (lr & 15)) * D + ((c4 ^ (lr & 7)) << 2));
+            if (to < 0) continue;
+            if (any_odd) {
+                const int node = (row0 + lr) / p.group;
 #pragma unroll 1
-                    for (int j = 0; j <= p.k; ++j) {
-                        if (j > 0 && (node == 0 || !((anc[node - 1] >> (j - 1)) & 1))) continue;
-                        const int page = table[(len + j) >> p.page_shift];
-                        const uint64_t at = row_at(page, len + j);
+                for (int j = 0; j <= p.k; ++j) {
+                    if (j > 0 && (node == 0 || !((anc[node - 1] >> (j - 1)) & 1))) continue;
+                    const uint64_t at = row_at(table[(len + j) >> p.page_shift], len + j);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint16_t x = vc[at * D + c4 * 4 + i];
-                            if (nonfinite16<F16>(x)) o[i] += from16<F16>(x);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint16_t x = vc[at * D + c4 * 4 + i];
+                        if (nonfinite16<F16>(x)) o[i] += from16<F16>(x);
                     }
                 }
-                if (whole) {
-                    if (row < p.rows) {
-                        const int head = h * p.group + row - node * p.group;
-                        const bool there = node == 0 || anc[node - 1] != 0;
-                        const int64_t at = (static_cast<int64_t>(b) * (p.k + 1) + node) * p.q_heads + head;
-                        const float inv = 1.f / ll;
-                        shortx4_t x;
+            }
+            if (whole) {
+                shortx4_t x;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = there ? to16<F16>(o[i] * inv) : short{0};
-                        *reinterpret_cast<shortx4_t*>(static_cast<uint16_t*>(p.out) + at * D + c4 * 4) = x;
-                        if (p.lse && c4 == 0)
-                            p.lse[at] = there ? (mm + __log2f(ll)) * 0.69314718055994531f : -__builtin_inff();
-                    }
-                } else {
-                    *reinterpret_cast<floatx4_t*>(p.part_acc + (slot * (MT * 16) + lr) * D + c4 * 4) = o;
-                    if (c4 == 0) {
-                        // rows of absent nodes are joined as having seen nothing
-                        const bool there = node == 0 || anc[node - 1] != 0;
-                        *reinterpret_cast<float2*>(p.part_ml + (slot * (MT * 16) + lr) * 2) =
-                            there ? float2{mm, ll} : float2{-__builtin_inff(), 0.f};
-                    }
-                }
+                for (int i = 0; i < 4; ++i) x[i] = f != 0.f ? to16<F16>(o[i] * f) : short{0};
+                *reinterpret_cast<shortx4_t*>(static_cast<uint16_t*>(p.out) + to * D + c4 * 4) = x;
+            } else {
+                *reinterpret_cast<floatx4_t*>(p.part_acc + to * D + c4 * 4) = o;
             }
         }
         __syncthreads();  // the buffers are free again
