@@ -22,6 +22,15 @@ constexpr int kCopyThreads = 256;
 constexpr int kBookThreads = 1024;  // the page bookkeeping runs in one workgroup
 constexpr int kBookWaves = kBookThreads / 64;
 
+// A barrier that the bookkeeping workgroup's stores and counts have passed:
+// they have reached the L2 that fresh() reads from.
+__device__ __forceinline__ void settle() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
+// A value that other threads of the workgroup may have changed, past the
+// compute unit's own cache.
 __device__ __forceinline__ int fresh(const int32_t* x) {
     return __hip_atomic_load(x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -196,8 +205,7 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
         }
         if (lane == 0) c.page_count[b] = static_cast<int>(t);
     }
-    __threadfence();
-    __syncthreads();
+    settle();
     int need = 0;
     for (int base = 0; base < c.n_seqs; base += kBookThreads) {
         const int b = base + threadIdx.x;
@@ -226,8 +234,7 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
         c.page_table[static_cast<int64_t>(lo) * c.max_pages + fresh(&c.page_count[lo]) + rank - begin_of(lo)] = id;
         c.page_refs[id] = 1;
     });
-    __threadfence();
-    __syncthreads();
+    settle();
     // Served are the sequences whose whole wish lies before the last free
     // page; the one that it falls into gives its part back.
     for (int b = wave; b < c.n_seqs; b += kBookWaves) {
@@ -247,60 +254,61 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
     }
 }
 
+// The pairs' claims, ranks and pages stay in LDS; only the copy list goes to
+// memory.  new_page of a pair: first the rank of its copy among all copies,
+// then the page (-1: nothing to copy, -2: the pair is refused).
 __global__ __launch_bounds__(kBookThreads) void k_cache_fork(ForkPlan p) {
+    __shared__ int claim[kCacheMaxSeqs];     // the first pair that names the sequence as its destination
+    __shared__ int new_page[kCacheMaxSeqs];
+    __shared__ int pair_of[kCacheMaxSeqs];   // the pair of each rank
     __shared__ int tmp[kBookWaves];
     const CachePlan& c = p.c;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int page_mask = (1 << c.page_shift) - 1;
     const auto in_range = [&](int s) { return s >= 0 && s < c.n_seqs; };
-    for (int i = threadIdx.x; i < p.n; i += kBookThreads) {
-        if (in_range(p.src[i])) p.claim[p.src[i]] = INT_MAX;
-        if (in_range(p.dst[i])) p.claim[p.dst[i]] = INT_MAX;
-    }
-    __threadfence();
+    for (int i = threadIdx.x; i < c.n_seqs; i += kBookThreads) claim[i] = INT_MAX;
     __syncthreads();
-    // The first pair that names a destination has it.
     for (int i = threadIdx.x; i < p.n; i += kBookThreads)
-        if (in_range(p.dst[i])) atomicMin(&p.claim[p.dst[i]], i);
-    __threadfence();
+        if (in_range(p.dst[i])) atomicMin(&claim[p.dst[i]], i);
     __syncthreads();
-    const auto usable = [&](int i) {
-        const int s = p.src[i], d = p.dst[i];
-        if (!in_range(s) || !in_range(d)) return false;
-        const int len = c.seq_len[s], have = c.page_count[s];
-        // a source that is a destination too would be read while it is written
-        return fresh(&p.claim[d]) == i && fresh(&p.claim[s]) == INT_MAX && c.page_count[d] == 0 && len >= 0 &&
-               have >= 0 && have <= c.max_pages && ((static_cast<int64_t>(len) + page_mask) >> c.page_shift) <= have;
-    };
-    // new_page[i]: the rank of the pair's copy among all copies, then its page
-    // (-1: nothing to copy, -2: the pair is refused).
     int need = 0;
     for (int base = 0; base < p.n; base += kBookThreads) {
         const int i = base + threadIdx.x;
-        const bool ok = i < p.n && usable(i);
-        const int more = ok && (c.seq_len[p.src[i]] & page_mask) != 0;
+        bool ok = false;
+        int len = 0;
+        if (i < p.n) {
+            const int s = p.src[i], d = p.dst[i];
+            // a source that is a destination too would be read while it is written
+            if (in_range(s) && in_range(d) && claim[d] == i && claim[s] == INT_MAX) {
+                len = c.seq_len[s];
+                const int have = c.page_count[s];
+                ok = c.page_count[d] == 0 && len >= 0 && have >= 0 && have <= c.max_pages &&
+                     ((static_cast<int64_t>(len) + page_mask) >> c.page_shift) <= have;
+            }
+        }
+        const int more = ok && (len & page_mask) != 0;
         int all;
         const int incl = book_scan(more, &all, tmp);
         if (i < p.n) {
-            p.new_page[i] = ok ? (more ? need + incl - 1 : -1) : -2;
-            if (more) p.old_page[need + incl - 1] = i;  // the pair of each rank, for now
+            new_page[i] = ok ? (more ? need + incl - 1 : -1) : -2;
+            if (more) pair_of[need + incl - 1] = i;
         }
         need += all;
     }
-    __threadfence();
     __syncthreads();
     const int found = free_pages(c, need, tmp, [&](int rank, int id) {
-        p.new_page[fresh(&p.old_page[rank])] = id;
+        new_page[pair_of[rank]] = id;
         c.page_refs[id] = 1;
     });
-    __threadfence();
     __syncthreads();
-    for (int r = found + threadIdx.x; r < need; r += kBookThreads) p.new_page[fresh(&p.old_page[r])] = -2;  // none left
-    __threadfence();
+    for (int r = found + threadIdx.x; r < need; r += kBookThreads) new_page[pair_of[r]] = -2;  // none left
     __syncthreads();
     for (int i = wave; i < p.n; i += kBookWaves) {
-        const int id = fresh(&p.new_page[i]);
-        if (lane == 0 && p.status) p.status[i] = id != -2;
+        const int id = new_page[i];
+        if (lane == 0) {
+            p.new_page[i] = id;
+            if (p.status) p.status[i] = id != -2;
+        }
         if (id == -2) {
             if (lane == 0) p.old_page[i] = -1;
             continue;

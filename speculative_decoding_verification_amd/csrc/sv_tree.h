@@ -146,7 +146,6 @@ struct ForkPlan {
     const int32_t* src;
     const int32_t* dst;
     int32_t* status;
-    int32_t* claim;          // workspace: [n_seqs]
     int32_t* new_page;       // workspace: [n]
     int32_t* old_page;       // workspace: [n]
     int32_t n;

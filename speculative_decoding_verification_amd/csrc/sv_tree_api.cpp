@@ -297,8 +297,7 @@ sv_status sv_cache_commit(const sv_cache_desc* desc, int32_t k, const int32_t* p
 size_t sv_cache_fork_workspace_bytes(const sv_cache_desc* desc, int32_t n) {
     sv::CachePlan c{};
     if (sv::plan_cache(desc, &c) != SV_OK || n < 0 || n > sv::kCacheMaxSeqs) return 0;
-    const size_t bytes = sv::align_up(static_cast<size_t>(c.n_seqs) * sizeof(int32_t)) +
-                         2 * sv::align_up(static_cast<size_t>(n) * sizeof(int32_t));
+    const size_t bytes = 2 * sv::align_up(static_cast<size_t>(n) * sizeof(int32_t));
     return bytes < sv::kAlign ? sv::kAlign : bytes;
 }
 
@@ -326,8 +325,6 @@ sv_status sv_cache_fork(const sv_cache_desc* desc, int32_t n, const int32_t* src
     p.dst = dst;
     p.status = status;
     char* base = static_cast<char*>(workspace);
-    p.claim = reinterpret_cast<int32_t*>(base);
-    base += sv::align_up(static_cast<size_t>(p.c.n_seqs) * sizeof(int32_t));
     p.new_page = reinterpret_cast<int32_t*>(base);
     p.old_page = reinterpret_cast<int32_t*>(base + sv::align_up(static_cast<size_t>(n) * sizeof(int32_t)));
     p.n = n;

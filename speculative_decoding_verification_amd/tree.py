@@ -94,15 +94,52 @@ def _workspace(pool, device, nbytes: int, given=None, own: bool = False):
     return pool.get(device, nbytes)
 
 
+_HERE = contextlib.nullcontext()
+_raw_stream = None
+
+
+def _stream_of(device, stream):
+    """The given stream, or the device's current one (by torch's raw query where
+    it has one: half the time of building a Stream object)."""
+    global _raw_stream
+    if stream is not None:
+        return stream
+    if _raw_stream is None:
+        raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = _stream_handle if raw is None else lambda d: raw(
+            _torch().cuda.current_device() if d.index is None else d.index)
+    return _raw_stream(device)
+
+
 def _on(device):
     """Makes `device` the current one (the library launches on the current
     device).  Host tensors end here: their addresses must not reach a kernel."""
     torch = _torch()
     if device.type != "cuda":
         raise ValueError("tensors must be on a HIP device, got %s" % device)
-    if device.index in (None, torch.cuda.current_device()):
-        return contextlib.nullcontext()
+    if device.index is None or device.index == torch.cuda.current_device():
+        return _HERE
     return torch.cuda.device(device)
+
+
+class _Plans(dict):
+    """Checked descriptors by the call's signature (shapes, strides, types,
+    devices): a call like an earlier one is not checked again.  Nothing of the
+    tensors themselves is kept."""
+
+    def keep(self, key, plan):
+        if len(self) >= 256:
+            self.clear()
+        self[key] = plan
+        return plan
+
+
+def _sig(*tensors):
+    """What the checks of a call look at."""
+    return tuple(None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors)
+
+
+_APPENDS, _COMMITS, _FORKS, _RESIZES = _Plans(), _Plans(), _Plans(), _Plans()
 
 
 def _cache_dtype(t) -> int:
@@ -203,7 +240,7 @@ class TreeAttention:
 
     def __call__(self, stream: Optional[int] = None) -> TreeAttentionOutput:
         with _on(self._device):
-            st = self._lib.sv_tree_attention(*self._args, _stream_handle(self._device) if stream is None else stream)
+            st = self._lib.sv_tree_attention(*self._args, _stream_of(self._device, stream))
         if st:
             raise SVError(st, "sv_tree_attention", self._lib)
         return TreeAttentionOutput(self.out, self.lse)
@@ -280,7 +317,7 @@ class TreeVerifier:
 
     def __call__(self, stream: Optional[int] = None) -> TreeVerifyOutput:
         with _on(self._device):
-            st = self._lib.sv_verify_tree(*self._args, _stream_handle(self._device) if stream is None else stream)
+            st = self._lib.sv_verify_tree(*self._args, _stream_of(self._device, stream))
         if st:
             raise SVError(st, "sv_verify_tree", self._lib)
         return TreeVerifyOutput(self.accepted_len, self.out_tokens, self.path)
@@ -300,13 +337,8 @@ def verify_tree(target, draft, draft_tokens, parents, uniforms, temperature: flo
                         workspace=workspace, _pool=_WS_TREE)()
 
 
-def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, *, count=None,
-                 stream: Optional[int] = None) -> None:
-    """sv_cache_append: rows j < count[b] of k_new, v_new [B][t][kv_heads]
-    [head_dim] (strides multiples of 8, head dimension contiguous) to positions
-    seq_len[b] + j of one layer's cache."""
+def _append_plan(k_new, v_new, k_cache, v_cache, page_table, seq_len, count):
     torch = _torch()
-    lib = load_library()
     device = k_cache.device
     _check_cache(k_cache, v_cache, layers=False)
     ks, vs = _rows_strides("k_new", k_new), _rows_strides("v_new", v_new)
@@ -325,23 +357,31 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, *, count=N
     _check_dev("seq_len", seq_len, device, torch.int32, (B,))
     if count is not None:
         _check_dev("count", count, device, torch.int32, (B,))
-    desc = _cache_desc(B, max_pages, k_cache, layers=False)
-    rows = CacheRows(t, *ks, *vs)
+    return _cache_desc(B, max_pages, k_cache, layers=False), CacheRows(t, *ks, *vs)
+
+
+def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, *, count=None,
+                 stream: Optional[int] = None) -> None:
+    """sv_cache_append: rows j < count[b] of k_new, v_new [B][t][kv_heads]
+    [head_dim] (strides multiples of 8, head dimension contiguous) to positions
+    seq_len[b] + j of one layer's cache."""
+    lib = load_library()
+    device = k_cache.device
+    key = _sig(k_new, v_new, k_cache, v_cache, page_table, seq_len, count)
+    plan = _APPENDS.get(key)
+    if plan is None:
+        plan = _APPENDS.keep(key, _append_plan(k_new, v_new, k_cache, v_cache, page_table, seq_len, count))
+    desc, rows = plan
     with _on(device):
         st = lib.sv_cache_append(ctypes.byref(desc), ctypes.byref(rows), _ptr(k_new), _ptr(v_new), _ptr(count),
                                  _ptr(page_table), _ptr(seq_len), _ptr(k_cache), _ptr(v_cache),
-                                 _stream_handle(device) if stream is None else stream)
+                                 _stream_of(device, stream))
     if st:
         raise SVError(st, "sv_cache_append", lib)
 
 
-def cache_commit(path, accepted_len, k_cache, v_cache, page_table, seq_len, *, new_len=None,
-                 stream: Optional[int] = None):
-    """sv_cache_commit: moves the accepted branch's rows (path [B][k], accepted_len
-    [B] of verify_tree) in every layer of k_cache, v_cache [layers][pages]... and
-    returns the new lengths (`new_len` if given; it must not be seq_len)."""
+def _commit_plan(path, accepted_len, k_cache, v_cache, page_table, seq_len, new_len):
     torch = _torch()
-    lib = load_library()
     device = k_cache.device
     _check_cache(k_cache, v_cache, layers=True)
     n, max_pages = _table_shape(page_table, device)
@@ -351,25 +391,35 @@ def cache_commit(path, accepted_len, k_cache, v_cache, page_table, seq_len, *, n
     _check_dev("path", path, device, torch.int32, (n, k))
     _check_dev("accepted_len", accepted_len, device, torch.int32, (n,))
     _check_dev("seq_len", seq_len, device, torch.int32, (n,))
-    if new_len is None:
-        new_len = torch.empty_like(seq_len)
     _check_dev("new_len", new_len, device, torch.int32, (n,))
-    desc = _cache_desc(n, max_pages, k_cache, layers=True)
+    return _cache_desc(n, max_pages, k_cache, layers=True), k
+
+
+def cache_commit(path, accepted_len, k_cache, v_cache, page_table, seq_len, *, new_len=None,
+                 stream: Optional[int] = None):
+    """sv_cache_commit: moves the accepted branch's rows (path [B][k], accepted_len
+    [B] of verify_tree) in every layer of k_cache, v_cache [layers][pages]... and
+    returns the new lengths (`new_len` if given; it must not be seq_len)."""
+    lib = load_library()
+    device = k_cache.device
+    if new_len is None:
+        new_len = _torch().empty_like(seq_len)
+    key = _sig(path, accepted_len, k_cache, v_cache, page_table, seq_len, new_len)
+    plan = _COMMITS.get(key)
+    if plan is None:
+        plan = _COMMITS.keep(key, _commit_plan(path, accepted_len, k_cache, v_cache, page_table, seq_len, new_len))
+    desc, k = plan
     with _on(device):
         st = lib.sv_cache_commit(ctypes.byref(desc), k, _ptr(path), _ptr(accepted_len), _ptr(page_table),
                                  _ptr(seq_len), _ptr(new_len), _ptr(k_cache), _ptr(v_cache),
-                                 _stream_handle(device) if stream is None else stream)
+                                 _stream_of(device, stream))
     if st:
         raise SVError(st, "sv_cache_commit", lib)
     return new_len
 
 
-def cache_fork(src, dst, k_cache, v_cache, page_table, page_count, page_refs, seq_len, *, status=None,
-               workspace=None, stream: Optional[int] = None):
-    """sv_cache_fork: sequence dst[i] continues src[i] (whole pages shared, a begun
-    one copied in every layer).  Returns status [n] int32 (1 done, 0 refused)."""
+def _fork_plan(lib, src, dst, k_cache, v_cache, page_table, page_count, page_refs, seq_len, status):
     torch = _torch()
-    lib = load_library()
     device = k_cache.device
     _check_cache(k_cache, v_cache, layers=True)
     m, max_pages = _table_shape(page_table, device)
@@ -381,20 +431,46 @@ def cache_fork(src, dst, k_cache, v_cache, page_table, page_count, page_refs, se
     _check_dev("page_count", page_count, device, torch.int32, (m,))
     _check_dev("page_refs", page_refs, device, torch.int32, (int(k_cache.shape[1]),))
     _check_dev("seq_len", seq_len, device, torch.int32, (m,))
-    if status is None:
-        status = torch.empty(n, dtype=torch.int32, device=device)
     _check_dev("status", status, device, torch.int32, (n,))
     desc = _cache_desc(m, max_pages, k_cache, layers=True)
-    nbytes = lib.sv_cache_fork_workspace_bytes(ctypes.byref(desc), n)
-    workspace = _workspace(_WS_PLAIN, device, max(nbytes, 256), workspace)
+    return desc, n, max(256, lib.sv_cache_fork_workspace_bytes(ctypes.byref(desc), n))
+
+
+def cache_fork(src, dst, k_cache, v_cache, page_table, page_count, page_refs, seq_len, *, status=None,
+               workspace=None, stream: Optional[int] = None):
+    """sv_cache_fork: sequence dst[i] continues src[i] (whole pages shared, a begun
+    one copied in every layer).  Returns status [n] int32 (1 done, 0 refused)."""
+    lib = load_library()
+    device = k_cache.device
+    if status is None:
+        status = _torch().empty_like(src)
+    key = _sig(src, dst, k_cache, v_cache, page_table, page_count, page_refs, seq_len, status)
+    plan = _FORKS.get(key)
+    if plan is None:
+        plan = _FORKS.keep(key, _fork_plan(lib, src, dst, k_cache, v_cache, page_table, page_count, page_refs,
+                                           seq_len, status))
+    desc, n, nbytes = plan
+    workspace = _workspace(_WS_PLAIN, device, nbytes, workspace)
     with _on(device):
         st = lib.sv_cache_fork(ctypes.byref(desc), n, _ptr(src), _ptr(dst), _ptr(page_table), _ptr(page_count),
                                _ptr(page_refs), _ptr(seq_len), _ptr(k_cache), _ptr(v_cache), _ptr(status),
                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                               _stream_handle(device) if stream is None else stream)
+                               _stream_of(device, stream))
     if st:
         raise SVError(st, "sv_cache_fork", lib)
     return status
+
+
+def _resize_plan(want_len, page_table, page_count, page_refs, status, page_size):
+    torch = _torch()
+    device = page_table.device
+    m, max_pages = _table_shape(page_table, device)
+    _check_dev("want_len", want_len, device, torch.int32, (m,))
+    _check_dev("page_count", page_count, device, torch.int32, (m,))
+    _check_dev("page_refs", page_refs, device, torch.int32)
+    _check_dev("status", status, device, torch.int32, (m,))
+    # the pages' contents are not touched: one head of eight stands for any shape
+    return CacheDesc(m, int(page_refs.numel()), int(page_size), max_pages, 1, 1, 8, SV_BF16)
 
 
 def cache_resize(want_len, page_table, page_count, page_refs, *, page_size: int, status=None,
@@ -402,21 +478,17 @@ def cache_resize(want_len, page_table, page_count, page_refs, *, page_size: int,
     """sv_cache_resize: gives every sequence the pages for want_len[b] positions
     (negative: as it is, 0: frees all).  Returns status [B] int32 (1 done, 0
     refused and unchanged)."""
-    torch = _torch()
     lib = load_library()
     device = page_table.device
-    m, max_pages = _table_shape(page_table, device)
-    _check_dev("want_len", want_len, device, torch.int32, (m,))
-    _check_dev("page_count", page_count, device, torch.int32, (m,))
-    _check_dev("page_refs", page_refs, device, torch.int32)
     if status is None:
-        status = torch.empty(m, dtype=torch.int32, device=device)
-    _check_dev("status", status, device, torch.int32, (m,))
-    # the pages' contents are not touched: one head of eight stands for any shape
-    desc = CacheDesc(m, int(page_refs.numel()), int(page_size), max_pages, 1, 1, 8, SV_BF16)
+        status = _torch().empty_like(want_len)
+    key = (_sig(want_len, page_table, page_count, page_refs, status), page_size)
+    desc = _RESIZES.get(key)
+    if desc is None:
+        desc = _RESIZES.keep(key, _resize_plan(want_len, page_table, page_count, page_refs, status, page_size))
     with _on(device):
         st = lib.sv_cache_resize(ctypes.byref(desc), _ptr(want_len), _ptr(page_table), _ptr(page_count),
-                                 _ptr(page_refs), _ptr(status), _stream_handle(device) if stream is None else stream)
+                                 _ptr(page_refs), _ptr(status), _stream_of(device, stream))
     if st:
         raise SVError(st, "sv_cache_resize", lib)
     return status
