@@ -67,8 +67,10 @@ hipError_t launch_tree_attention(const AttnPlan& p, hipStream_t stream);
 constexpr int kTreeThreads = 512;
 constexpr int kTreeMaxSlices = 64;
 constexpr int kTreeMaxBatch = 65535;
-constexpr int kTreeWgs = 1024;   // workgroups of one pass, about
-constexpr int kTreePasses = 8;   // passes by several workgroups per sequence before one finishes the walk
+constexpr int kTreeWgs = 512;    // workgroups of a walk's pass: as many as run at once
+constexpr int kTreeRowWgs = 1024;  // workgroups that read every row at once, about
+constexpr int kTreeDies = 8;
+constexpr uint64_t kTreeWaitTicks = 2000000;  // of 10 ns: how long a workgroup waits for the others of its sequence
 constexpr int kTreeTile = kTreeThreads * 8;  // tokens one workgroup takes at a time
 constexpr int64_t kTreeAllRows = int64_t{48} << 20;  // logits up to which every row is read at once
 
@@ -95,9 +97,12 @@ struct TreePlan {
     int32_t* accepted_len;
     int32_t* out_tokens;
     int32_t* path;
-    uint32_t* arrived;           // [kTreeMaxBatch]: workgroups that have handed in a pass's partial; 0 between passes
-    TreeState* state;            // [B]: written by a call's first pass before its second reads it
-    double* part;                // [B][kTreeMaxSlices][4]: one pass's partials
+    // Left at 0 by every call, at the same place whatever its shape:
+    uint32_t* arrived;           // [kTreeMaxBatch]: workgroups that have handed in a row's partial
+    uint32_t* finished;          // [kTreeMaxBatch]: the sequence's outputs are written
+    uint64_t* exchange;          // [kTreeWgs][2][4]: partials of a walk's passes, tagged
+    // Written by a call before it is read:
+    TreeState* state;            // [B]
     double* row_part;            // [B][k+1+draft_rows][kTreeMaxSlices][2]: every row's, or NULL (rows read as the walk comes to them)
     int64_t per, row_per;        // tokens of one slice: of a pass, and where every row is read at once
     int32_t slices, row_slices;  // workgroups on one row
@@ -105,6 +110,7 @@ struct TreePlan {
     int32_t kind;                // TreeKind
     int32_t elem_bytes;          // 4 fp32, 2 bf16
     int32_t vec;                 // rows start on 16-byte boundaries
+    uint64_t wait_ticks;
     double c2;                   // log2(e) / T
 };
 

@@ -78,14 +78,16 @@ size_t attention_bytes(const AttnPlan& p) {
            align_up(static_cast<size_t>(p.clusters) * p.row_units * sizeof(AttnSplit));
 }
 
-// As many slices of whole tiles to a row as make about kTreeWgs workgroups on `rows` rows.
-void tree_slices(int64_t vocab, int64_t rows, int64_t* per, int32_t* slices) {
+// As many slices of whole tiles to a row as make up to `wgs` workgroups on `rows` rows.
+void tree_slices(int64_t vocab, int64_t rows, int64_t wgs, int64_t* per, int32_t* slices) {
     const int64_t tiles = (vocab + kTreeTile - 1) / kTreeTile;
     int64_t n = (tiles + kTreeMaxSlices - 1) / kTreeMaxSlices;
-    while (n < tiles && (tiles + n - 1) / n * rows > kTreeWgs) ++n;
+    while (n < tiles && (tiles + n - 1) / n * rows > wgs) ++n;
     *per = n * kTreeTile;
     *slices = static_cast<int32_t>((tiles + n - 1) / n);
 }
+
+uint64_t tree_wait_ticks = kTreeWaitTicks;  // tests set it to 0
 
 sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     if (!d) return SV_ERR_NULL_ARG;
@@ -102,19 +104,20 @@ sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     p->draft_rows = p->kind == kTreeLogits ? d->draft_rows : 0;
     p->elem_bytes = d->dtype == SV_BF16 ? 2 : 4;
     p->c2 = t == 0.f ? 0.0 : kLog2E / static_cast<double>(t);
-    tree_slices(p->vocab, p->batch, &p->per, &p->slices);
-    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows), &p->row_per, &p->row_slices);
+    tree_slices(p->vocab, p->batch, kTreeWgs, &p->per, &p->slices);
+    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows), kTreeRowWgs, &p->row_per,
+                &p->row_slices);
+    p->wait_ticks = tree_wait_ticks;
     return SV_OK;
 }
 
 size_t tree_state_bytes(int64_t batch) { return align_up(static_cast<size_t>(batch) * sizeof(TreeState)); }
 
-// The arrival counts are what one call leaves to the next (all 0), so they
-// stand at the same place whatever the shape: words of another call's shape
-// never lie where counts are.
+// What one call leaves to the next (all 0) stands at the same place whatever
+// the shape: words of another call's shape never lie there.
 constexpr size_t kTreeCountBytes = (static_cast<size_t>(kTreeMaxBatch) * sizeof(uint32_t) + kAlign - 1) & ~(kAlign - 1);
-
-size_t tree_part_bytes(int64_t batch) { return align_up(static_cast<size_t>(batch) * kTreeMaxSlices * 4 * sizeof(double)); }
+constexpr size_t kTreeExchangeBytes = static_cast<size_t>(kTreeWgs) * 8 * sizeof(uint64_t);
+constexpr size_t kTreeZeroBytes = 2 * kTreeCountBytes + kTreeExchangeBytes;
 
 // Whether the statistics of every row are taken at once.
 bool all_rows(const TreePlan& p) {
@@ -122,7 +125,7 @@ bool all_rows(const TreePlan& p) {
 }
 
 size_t tree_bytes(const TreePlan& p) {
-    size_t n = kTreeCountBytes + tree_state_bytes(p.batch) + tree_part_bytes(p.batch);
+    size_t n = kTreeZeroBytes + tree_state_bytes(p.batch);
     if (all_rows(p))
         n += align_up(static_cast<size_t>(p.batch) * (p.k + 1 + p.draft_rows) * kTreeMaxSlices * 2 * sizeof(double));
     return n;
@@ -198,6 +201,9 @@ sv_status sv_tree_attention(const sv_tree_attention_desc* desc, const void* q, c
     return sv::launched(sv::launch_tree_attention(p, stream));
 }
 
+// For tests of what follows a wait that ran out: the longest wait, in 10 ns.
+void sv_internal_tree_wait(uint64_t ticks) { sv::tree_wait_ticks = ticks; }
+
 size_t sv_verify_tree_workspace_bytes(const sv_verify_tree_desc* desc) {
     sv::TreePlan p{};
     return sv::plan_tree(desc, &p) == SV_OK ? sv::tree_bytes(p) : 0;
@@ -227,12 +233,13 @@ sv_status sv_verify_tree(const sv_verify_tree_desc* desc, const void* target_log
     p.accepted_len = accepted_len;
     p.out_tokens = out_tokens;
     p.path = path_out;
-    p.arrived = static_cast<uint32_t*>(workspace);
-    char* base = static_cast<char*>(workspace) + sv::kTreeCountBytes;
+    char* base = static_cast<char*>(workspace);
+    p.arrived = reinterpret_cast<uint32_t*>(base);
+    p.finished = reinterpret_cast<uint32_t*>(base + sv::kTreeCountBytes);
+    p.exchange = reinterpret_cast<uint64_t*>(base + 2 * sv::kTreeCountBytes);
+    base += sv::kTreeZeroBytes;
     p.state = reinterpret_cast<sv::TreeState*>(base);
-    base += sv::tree_state_bytes(p.batch);
-    p.part = reinterpret_cast<double*>(base);
-    p.row_part = sv::all_rows(p) ? reinterpret_cast<double*>(base + sv::tree_part_bytes(p.batch)) : nullptr;
+    p.row_part = sv::all_rows(p) ? reinterpret_cast<double*>(base + sv::tree_state_bytes(p.batch)) : nullptr;
     p.vec = static_cast<int64_t>(p.vocab) * p.elem_bytes % 16 == 0 && sv::aligned(target_logits, 16) &&
             (!p.draft || sv::aligned(p.draft, 16));
     return sv::launched(sv::launch_verify_tree(p, stream));

@@ -29,7 +29,6 @@
 // Only the rows on the walked path are read.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <climits>
 #include <cstdint>
 
@@ -79,7 +78,7 @@ struct Power {
 __device__ __forceinline__ double power_of(float top, double c2) {
     const double y = static_cast<double>(top) * c2;
     // finite rows give finite bounds; an empty part of a row, or a part of -inf alone, gives 0
-    return y >= -9e14 && y <= 9e14 ? __builtin_ceil(y) : 0.0;
+    return y >= -8e12 && y <= 8e12 ? __builtin_ceil(y) : 0.0;
 }
 
 // x 2^(m - top), m <= top whole numbers.
@@ -181,6 +180,14 @@ __device__ __forceinline__ double join(bool mine, double m, double z, double* m_
     return s;
 }
 
+// What a complete pass leads to.
+struct Next {
+    bool draw;         // a token is due: from the tokens [from, from + len), `run` the mass before them
+    int best;          // greedy: the token
+    int64_t from, len;
+    double run, goal;
+};
+
 constexpr int kGroup = 16;  // bytes of registers / 2 that a group of tiles takes: 8 tiles of 16-bit, 4 of 32-bit elements
 
 struct Shared {
@@ -189,11 +196,11 @@ struct Shared {
     int wave_i[NWAVES];
     double bcast[8];
     int ibcast[8];
-    int64_t lcast[2];
     int gone[SV_MAX_DRAFT];  // one-hot: the rejected siblings' tokens and their p
     double gone_p[SV_MAX_DRAFT];
     int n_gone;
     TreeState st;
+    Next nx;
 };
 
 // Sum over the workgroup, on every thread, in a fixed order.
@@ -443,8 +450,9 @@ __device__ __forceinline__ Node node_of(const TreePlan& p, int b) {
 // The walk's next decision, taken by the first wavefront.  On entry st holds
 // the row's statistics (or F(t)); on return its stage says what is needed next,
 // and the answer is true when a token is to be drawn from what is left at st.at.
+// Every workgroup of a sequence may take the decision, one (`lead`) writes it.
 template <int KIND>
-__device__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st, int argmax, Shared& sh) {
+__device__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
     const bool child = (st.left >> lane) & 1;
@@ -500,7 +508,7 @@ __device__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st
     }
     if (hit >= 0) {
         const int x = __shfl(node.tok, hit);
-        if (lane == 0) {
+        if (lead && lane == 0) {
             p.path[bk + st.kept] = hit;
             p.out_tokens[bk + b + st.kept] = x;
         }
@@ -613,102 +621,82 @@ __device__ __forceinline__ bool fits(const TreePlan& p, int b, const Node& node,
     return start.stage != kStageDone && (st.left & ~__ballot(node.up == st.at)) == 0;
 }
 
-// Goes on with a walk whose pass is complete: the first wavefront decides as
-// far as what is known reaches, the workgroup draws where a token is due.  r:
-// the pass's partials, lane i's of slice i (only the first wavefront's count).
-// With p.row_part the statistics of every row are there already, and only a
-// residual's mass needs another pass.  Returns the state for the next pass.
+// Goes on with a walk whose pass is complete, as far as what is known reaches
+// (the first wavefront).  r: the pass's partials, lane i's of slice i.  With
+// p.row_part the statistics of every row are there already, and only a
+// residual's mass needs another pass.  st is what the next pass works on.
 template <typename T, int KIND>
-__device__ void go_on(const TreePlan& p, int b, const Node& node, TreeState st, double (&r)[4], Shared& sh) {
-    const int tid = threadIdx.x, lane = tid & 63;
+__device__ Next go_on(const TreePlan& p, int b, const Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
+    const int lane = threadIdx.x & 63;
     const bool by_rows = p.row_part && st.stage == kStageRow;
     int slices = by_rows ? p.row_slices : p.slices;
     int64_t per = by_rows ? p.row_per : p.per;
-    if (tid < 64) {
-        int best = 0;
-        double mass = 0.0;  // of this lane's slice
-        bool draw = false;
-        while (true) {
-            if (p.row_part && st.stage == kStageRow) {
-                slices = p.row_slices;
-                per = p.row_per;
-                const int rows = p.k + 1 + p.draft_rows;
-                const double* const at = p.row_part + (static_cast<int64_t>(b) * rows * kTreeMaxSlices + lane) * 2;
-                const int64_t tr = static_cast<int64_t>(st.at + 1) * kTreeMaxSlices * 2;
-                const int64_t dr = static_cast<int64_t>(p.k + 1 + st.at + 1) * kTreeMaxSlices * 2;
-                if (lane < slices) {
-                    r[0] = taken(at + tr);
-                    r[1] = taken(at + tr + 1);
-                    if (KIND == kTreeLogits && st.left) {
-                        r[2] = taken(at + dr);
-                        r[3] = taken(at + dr + 1);
-                    }
+    Next nx{false, 0, 0, 0, 0.0, 0.0};
+    double mass = 0.0;  // of this lane's slice
+    while (true) {
+        if (p.row_part && st.stage == kStageRow) {
+            slices = p.row_slices;
+            per = p.row_per;
+            const int rows = p.k + 1 + p.draft_rows;
+            const double* const at = p.row_part + (static_cast<int64_t>(b) * rows * kTreeMaxSlices + lane) * 2;
+            const int64_t tr = static_cast<int64_t>(st.at + 1) * kTreeMaxSlices * 2;
+            const int64_t dr = static_cast<int64_t>(p.k + 1 + st.at + 1) * kTreeMaxSlices * 2;
+            if (lane < slices) {
+                r[0] = taken(at + tr);
+                r[1] = taken(at + tr + 1);
+                if (KIND == kTreeLogits && st.left) {
+                    r[2] = taken(at + dr);
+                    r[3] = taken(at + dr + 1);
                 }
             }
-            if (KIND == kTreeGreedy) {
-                float m = lane < slices ? static_cast<float>(r[0]) : -__builtin_inff();
-                best = lane < slices ? static_cast<int>(r[1]) : INT_MAX;
-                wave_argmax(m, best);
-            } else if (st.stage == kStageRow) {
-                mass = join(lane < slices, r[0], r[1], &st.m_t, &st.z_t) / st.z_t;
-                if (KIND == kTreeLogits && st.left) join(lane < slices, r[2], r[3], &st.m_q, &st.z_q);
-            } else {
-                mass = lane < slices ? r[0] : 0.0;
-                st.f = wave_sum(mass);
-            }
-            draw = decide<KIND>(p, b, node, st, best, sh);
-            if (draw || !p.row_part || st.stage != kStageRow) break;
         }
-        if (draw && KIND != kTreeGreedy) {
-            if (KIND == kTreeOneHot) mass = __builtin_fmax(0.0, mass - gone_mass(sh, lane * per, (lane + 1) * per));
-            if (lane >= slices) mass = 0.0;
-            double cum = mass;
+        if (KIND == kTreeGreedy) {
+            float m = lane < slices ? static_cast<float>(r[0]) : -__builtin_inff();
+            nx.best = lane < slices ? static_cast<int>(r[1]) : INT_MAX;
+            wave_argmax(m, nx.best);
+        } else if (st.stage == kStageRow) {
+            mass = join(lane < slices, r[0], r[1], &st.m_t, &st.z_t) / st.z_t;
+            if (KIND == kTreeLogits && st.left) join(lane < slices, r[2], r[3], &st.m_q, &st.z_q);
+        } else {
+            mass = lane < slices ? r[0] : 0.0;
+            st.f = wave_sum(mass);
+        }
+        nx.draw = decide<KIND>(p, b, node, st, nx.best, lead, sh);
+        if (nx.draw || !p.row_part || st.stage != kStageRow) break;
+    }
+    if (nx.draw && KIND != kTreeGreedy) {
+        if (KIND == kTreeOneHot) mass = __builtin_fmax(0.0, mass - gone_mass(sh, lane * per, (lane + 1) * per));
+        if (lane >= slices) mass = 0.0;
+        double cum = mass;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double o = __shfl_up(cum, d);
-                if (lane >= d) cum += o;
-            }
-            const double goal = static_cast<double>(p.uniforms[static_cast<int64_t>(b) * (p.k + 1) + p.k]) * __shfl(cum, 63);
-            uint64_t past = __ballot(mass > 0.0 && cum > goal);
-            if (!past) {  // rounding left none: the last slice that holds anything
-                const uint64_t any = __ballot(mass > 0.0);
-                past = any ? uint64_t{1} << (63 - __builtin_clzll(any)) : 1;
-            }
-            const int at = __builtin_ctzll(past);
-            const double run = __shfl(cum - mass, at);
-            if (lane == 0) {
-                sh.bcast[0] = run;
-                sh.bcast[1] = goal;
-                sh.lcast[0] = at * per;
-                sh.lcast[1] = per;
-            }
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_up(cum, d);
+            if (lane >= d) cum += o;
         }
-        if (lane == 0) {
-            sh.st = st;
-            sh.ibcast[1] = draw;
-            sh.ibcast[4] = best;
+        nx.goal = static_cast<double>(p.uniforms[static_cast<int64_t>(b) * (p.k + 1) + p.k]) * __shfl(cum, 63);
+        uint64_t past = __ballot(mass > 0.0 && cum > nx.goal);
+        if (!past) {  // rounding left none: the last slice that holds anything
+            const uint64_t any = __ballot(mass > 0.0);
+            past = any ? uint64_t{1} << (63 - __builtin_clzll(any)) : 1;
         }
+        const int at = __builtin_ctzll(past);
+        nx.run = __shfl(cum - mass, at);
+        nx.from = at * per;
+        nx.len = per;
     }
-    __syncthreads();
-    const bool draw = sh.ibcast[1];
-    if (draw) {
-        st = sh.st;
-        int y = sh.ibcast[4];
-        if (KIND != kTreeGreedy) {
-            const Rows<T, KIND> rows(p, b, st);
-            const int64_t from = sh.lcast[0];
-            y = slice_draw(rows.target, st.stage == kStageMass ? rows.draft : static_cast<const T*>(nullptr), from,
-                           min(static_cast<int64_t>(p.vocab), from + sh.lcast[1]), p.vec != 0, p.c2, st, sh.bcast[0],
-                           sh.bcast[1], sh);
-        }
-        if (tid < 64) finish(p, b, st, y);
+    return nx;
+}
+
+// The token that is due, and the sequence's end (the whole workgroup).
+template <typename T, int KIND>
+__device__ void draw_token(const TreePlan& p, int b, const TreeState& st, const Next& nx, Shared& sh) {
+    int y = nx.best;
+    if (KIND != kTreeGreedy) {
+        const Rows<T, KIND> rows(p, b, st);
+        y = slice_draw(rows.target, st.stage == kStageMass ? rows.draft : static_cast<const T*>(nullptr), nx.from,
+                       min(static_cast<int64_t>(p.vocab), nx.from + nx.len), p.vec != 0, p.c2, st, nx.run, nx.goal, sh);
     }
-    if (tid == 0) {
-        TreeState next = sh.st;
-        p.arrived[b] = 0;
-        if (draw) next.stage = kStageDone;
-        p.state[b] = next;
-    }
+    if (threadIdx.x < 64) finish(p, b, st, y);
 }
 
 // The statistics of every row of the tree at once; the last workgroup of a
@@ -757,27 +745,52 @@ __global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
     if (tid < 64) {
         node = node_of<T, KIND>(p, b);
         begin<KIND>(p, b, node, st);
+        Next nx{false, 0, 0, 0, 0.0, 0.0};
         if (st.stage == kStageDone) refuse(p, b);
+        else nx = go_on<T, KIND>(p, b, node, st, r, true, sh);
         if (tid == 0) {
             sh.st = st;
-            if (st.stage == kStageDone) {
-                p.state[b] = st;
-                p.arrived[b] = 0;
-            }
+            sh.nx = nx;
         }
     }
     __syncthreads();
     st = sh.st;
-    if (st.stage == kStageDone) return;
-    go_on<T, KIND>(p, b, node, st, r, sh);
+    const Next nx = sh.nx;
+    if (nx.draw) draw_token<T, KIND>(p, b, st, nx, sh);
+    if (tid == 0) {
+        p.arrived[b] = 0;
+        if (KIND == kTreeLogits) {  // the kernels that follow go on with it
+            p.state[b] = st;
+            p.finished[b] = nx.draw || st.stage == kStageDone;
+        }
+    }
 }
 
-// What a sequence's walk needs next, worked out by p.slices workgroups, each
-// on its part of the vocabulary; the last one to hand in its part goes on.
+// A value handed to the other workgroups: its low byte (2^-44 of it) is the
+// pass's number, so that a word tells by itself whether it is this pass's.
+__device__ __forceinline__ uint64_t tagged(double x, uint32_t pass) {
+    return (static_cast<uint64_t>(__double_as_longlong(x)) & ~uint64_t{255}) | pass;
+}
+
+// The walks, p.slices workgroups to a sequence, each on its part of the
+// vocabulary.  After each pass every workgroup reads the others' partials and
+// takes the same decision from them, so nothing goes through memory but the
+// partials, once; the one in whose part the token lies draws it.
+//
+// Waiting.  A sequence's workgroups have consecutive places on one die, whose
+// dispatch is in order, so they come to run whatever else does.  Nothing
+// depends on it: the wait is bounded (p.wait_ticks of 10 ns), a workgroup that
+// gives up leaves, the first one leaves the state behind, and k_tree_walk ends
+// the walk from there.
 template <typename T, int KIND>
-__global__ __launch_bounds__(NT) void k_tree_pass(TreePlan p, int first) {
+__global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
     __shared__ Shared sh;
-    const int b = blockIdx.y, slice = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int die = blockIdx.x % kTreeDies, on_die = blockIdx.x / kTreeDies;
+    const int b = on_die / p.slices * kTreeDies + die, slice = on_die % p.slices;
+    if (b >= p.batch) return;
+    if (!first && p.finished[b]) return;
+    const bool lead = slice == 0;
     TreeState st{};
     if (first) {  // at the root; whether it has children is seen later
         st.at = -1;
@@ -785,52 +798,110 @@ __global__ __launch_bounds__(NT) void k_tree_pass(TreePlan p, int first) {
         st.stage = kStageRow;
     } else {
         st = p.state[b];
-        if (!in_range<KIND>(p, st)) return;  // done, mostly
+        if (!in_range<KIND>(p, st)) return;
     }
     Node node{};
-    if (tid < 64) node = node_of<T, KIND>(p, b);
-    if (tid == 0) sh.n_gone = 0;
-    const int64_t V = p.vocab, lo = slice * p.per, hi = min(V, lo + p.per);
-    const bool vec = p.vec != 0;
-    const Rows<T, KIND> rows(p, b, st);
-    double* const part = p.part + static_cast<int64_t>(b) * kTreeMaxSlices * 4;
-    double r[4] = {0.0, 0.0, 0.0, 0.0};
-    if (KIND == kTreeGreedy) {
-        float m;
-        int at;
-        slice_argmax(rows.target, lo, hi, vec, sh, &m, &at);
-        r[0] = m;
-        r[1] = at;
-    } else if (st.stage == kStageRow) {
-        slice_stats(rows.target, lo, hi, vec, p.c2, sh, &r[0], &r[1]);
-        if (rows.draft) slice_stats(rows.draft, lo, hi, vec, p.c2, sh, &r[2], &r[3]);
-    } else {
-        r[0] = slice_mass(rows.target, rows.draft, lo, hi, vec, p.c2, st, sh);
-    }
-    if (tid == 0) sh.ibcast[2] = hand_in(part + slice * 4, r, 4, &p.arrived[b], p.slices);
-    __syncthreads();
-    if (!sh.ibcast[2]) return;
     if (tid < 64) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = tid < p.slices ? taken(part + tid * 4 + i) : 0.0;
+        node = node_of<T, KIND>(p, b);
         if (first) {
             begin<KIND>(p, b, node, st);
-            if (st.stage == kStageDone) refuse(p, b);
+            if (st.stage == kStageDone && lead) {
+                refuse(p, b);
+                if (tid == 0) p.finished[b] = 1;
+            }
         } else if (!fits<KIND>(p, b, node, st)) {
             st.stage = kStageDone;
         }
         if (tid == 0) {
             sh.st = st;
-            if (st.stage == kStageDone) {
-                p.state[b] = st;
-                p.arrived[b] = 0;
-            }
+            sh.n_gone = 0;
         }
     }
+    const int64_t V = p.vocab, lo = slice * p.per, hi = min(V, lo + p.per);
+    const bool vec = p.vec != 0;
+    uint64_t* const words = p.exchange + (static_cast<int64_t>(b) * p.slices) * 8;
     __syncthreads();
-    st = sh.st;
-    if (st.stage == kStageDone) return;
-    go_on<T, KIND>(p, b, node, st, r, sh);
+    for (uint32_t pass = 1; pass <= SV_MAX_DRAFT + 1u; ++pass) {
+        st = sh.st;
+        if (st.stage == kStageDone) return;  // a refused tree
+        const Rows<T, KIND> rows(p, b, st);
+        double r[4] = {0.0, 0.0, 0.0, 0.0};
+        int n = KIND == kTreeGreedy || st.stage == kStageMass ? 1 : rows.draft ? 4 : 2;
+        float best_m = 0.f;
+        int best_at = 0;
+        if (KIND == kTreeGreedy) {
+            slice_argmax(rows.target, lo, hi, vec, sh, &best_m, &best_at);
+        } else if (st.stage == kStageRow) {
+            slice_stats(rows.target, lo, hi, vec, p.c2, sh, &r[0], &r[1]);
+            if (rows.draft) slice_stats(rows.draft, lo, hi, vec, p.c2, sh, &r[2], &r[3]);
+        } else {
+            r[0] = slice_mass(rows.target, rows.draft, lo, hi, vec, p.c2, st, sh);
+        }
+        if (tid < 64) {
+            // Two sets of words in turn: a workgroup is at most one pass ahead
+            // of the slowest, which still reads the other set.
+            uint64_t* const set = words + (pass & 1) * 4;
+            if (tid == 0) {
+                if (KIND == kTreeGreedy) {
+                    // an empty slice's index (all ones) is past every token
+                    const uint64_t w = static_cast<uint64_t>(__float_as_uint(best_m)) << 32 |
+                                       static_cast<uint64_t>(min(best_at, 0xFFFFFF)) << 8 | pass;
+                    __hip_atomic_store(set + slice * 8, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n)
+                            __hip_atomic_store(set + slice * 8 + i, tagged(r[i], pass), __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+                }
+            }
+            const uint64_t began = __builtin_amdgcn_s_memrealtime();
+            bool here = false;
+            uint64_t w[4] = {0, 0, 0, 0};
+            while (true) {
+                bool ok = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n && lane < p.slices) {
+                        w[i] = __hip_atomic_load(set + lane * 8 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                        ok = ok && (w[i] & 255) == pass;
+                    }
+                here = __all(ok);
+                if (here || __builtin_amdgcn_s_memrealtime() - began > p.wait_ticks) break;
+                __builtin_amdgcn_s_sleep(1);
+            }
+            Next nx{false, 0, 0, 0, 0.0, 0.0};
+            const TreeState before = st;
+            if (here) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = __longlong_as_double(static_cast<long long>(w[i] & ~uint64_t{255}));
+                if (KIND == kTreeGreedy) {
+                    r[0] = __uint_as_float(static_cast<uint32_t>(w[0] >> 32));
+                    r[1] = static_cast<double>((w[0] >> 8) & 0xFFFFFF);
+                }
+                nx = go_on<T, KIND>(p, b, node, st, r, lead, sh);
+            }
+            if (tid == 0) {
+                sh.st = st;
+                sh.nx = nx;
+                sh.ibcast[1] = here;
+                // what the walk goes on from, should this pass or the draw not be ended here
+                if (lead && (!here || nx.draw)) p.state[b] = here ? st : before;
+            }
+        }
+        __syncthreads();
+        if (!sh.ibcast[1]) return;
+        const Next nx = sh.nx;
+        if (nx.draw) {
+            const bool mine = KIND == kTreeGreedy ? lead : slice == nx.from / p.per;
+            if (mine) {
+                st = sh.st;
+                draw_token<T, KIND>(p, b, st, nx, sh);
+                if (tid == 0) p.finished[b] = 1;
+            }
+            return;
+        }
+    }
 }
 
 // The rest of a walk (all of it where no pass came before) by one workgroup
@@ -842,21 +913,21 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
     const int64_t V = p.vocab;
     const bool vec = p.vec != 0;
     Node node{};
+    if (!first) {  // the workspace as the next call expects it
+        const bool done = p.finished[b] != 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.slices * 8; i += NT) p.exchange[static_cast<int64_t>(b) * p.slices * 8 + i] = 0;
+        if (threadIdx.x == 0) p.finished[b] = 0;
+        if (done) return;
+    }
     if (threadIdx.x < 64) {
         TreeState st{};
-        if (first) {
-            node = node_of<T, KIND>(p, b);
-            begin<KIND>(p, b, node, st);
-        } else {
-            st = p.state[b];
-            if (in_range<KIND>(p, st)) {
-                node = node_of<T, KIND>(p, b);
-                if (!fits<KIND>(p, b, node, st)) st.stage = kStageDone;
-            } else {
-                st.stage = kStageDone;
-            }
-        }
+        if (!first) st = p.state[b];
+        const bool ranged = first || in_range<KIND>(p, st);
+        if (ranged) node = node_of<T, KIND>(p, b);
+        if (first) begin<KIND>(p, b, node, st);
         if (first && st.stage == kStageDone) refuse(p, b);
+        if (!first && (!ranged || !fits<KIND>(p, b, node, st))) st.stage = kStageDone;
         if (threadIdx.x == 0) {
             sh.st = st;
             sh.n_gone = 0;
@@ -879,7 +950,7 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
         }
         __syncthreads();
         if (threadIdx.x < 64) {
-            const bool draw = decide<KIND>(p, b, node, st, best, sh);
+            const bool draw = decide<KIND>(p, b, node, st, best, true, sh);
             if (threadIdx.x == 0) {
                 sh.st = st;
                 sh.ibcast[1] = draw;
@@ -906,18 +977,15 @@ hipError_t launch_kind(const TreePlan& p, hipStream_t stream) {
         k_tree_walk<T, KIND><<<p.batch, NT, 0, stream>>>(p, 1);
         return hipGetLastError();
     }
-    int passes = std::min(p.k + 1, kTreePasses);
     if (p.row_part) {
         k_tree_rows<T, KIND><<<dim3(p.row_slices, p.k + 1 + p.draft_rows, p.batch), NT, 0, stream>>>(p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || KIND != kTreeLogits) return e;
-        passes = std::min(p.k, kTreePasses);
     }
-    for (int i = 0; i < passes; ++i) {
-        k_tree_pass<T, KIND><<<dim3(p.slices, p.batch), NT, 0, stream>>>(p, i == 0 && !p.row_part);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+    const int blocks = (p.batch + kTreeDies - 1) / kTreeDies * kTreeDies * p.slices;
+    k_tree_cluster<T, KIND><<<blocks, NT, 0, stream>>>(p, !p.row_part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     k_tree_walk<T, KIND><<<p.batch, NT, 0, stream>>>(p, 0);
     return hipGetLastError();
 }

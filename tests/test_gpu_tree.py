@@ -452,6 +452,48 @@ def test_walk_calls_of_other_shapes_on_one_workspace(dev):
         assert int(got.accepted_len.min()) >= 0
 
 
+@pytest.mark.parametrize("onehot", [False, True], ids=["logits", "onehot"])
+@pytest.mark.parametrize("T", [0.0, 1.0])
+def test_walk_when_no_workgroup_waits(dev, onehot, T):
+    """The longest wait set to nothing: workgroups leave before the others' parts are there, and the walks are ended by
+    the kernel that follows, with the same results; the workspace serves the next call as ever."""
+    import ctypes
+
+    lib = sv.load_library()
+    lib.sv_internal_tree_wait.argtypes = [ctypes.c_uint64]
+    cases = [logits_case(B, B, k, V, T, onehot) for B, k, V in ((40, 12, 30000), (3, 20, 9000), (100, 5, 20000))]
+    on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
+    args = [tuple(on(x) for x in c) for c in cases]
+    want = [[x.clone() for x in sv.verify_tree(*a, T, onehot=onehot)] for a in args]
+    try:
+        for ticks in (0, 200):
+            lib.sv_internal_tree_wait(ticks)
+            for a, w in zip(args, want):
+                got = sv.verify_tree(*a, T, onehot=onehot)
+                torch.cuda.synchronize()
+                assert all(torch.equal(x, y) for x, y in zip(got, w))
+    finally:
+        lib.sv_internal_tree_wait(2000000)
+    for a, w in zip(args, want):
+        assert all(torch.equal(x, y) for x, y in zip(sv.verify_tree(*a, T, onehot=onehot), w))
+
+
+def test_walks_on_two_streams_at_once(dev):
+    on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
+    cases = [tuple(on(x) for x in logits_case(i, 120, 8, 40000, 1.0, False)) for i in range(2)]
+    want = [[x.clone() for x in sv.verify_tree(*c, 1.0)] for c in cases]
+    calls = [sv.TreeVerifier(*c, 1.0) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for call, st in zip(calls, streams):
+            call(stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for call, w in zip(calls, want):
+        got = (call.accepted_len, call.out_tokens, call.path)
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
+
+
 # ------------------------------------------------------------------------------------------------------- the cache
 
 def same_bits(a, b):
