@@ -121,7 +121,8 @@ constexpr size_t kTreeZeroBytes = 2 * kTreeCountBytes + kTreeExchangeBytes;
 
 // Whether the statistics of every row are taken at once.
 bool all_rows(const TreePlan& p) {
-    return p.slices > 1 && static_cast<int64_t>(p.batch) * (p.k + 1 + p.draft_rows) * p.vocab <= kTreeAllRows;
+    const int64_t most = p.kind == kTreeGreedy ? kTreeAllRowsGreedy : kTreeAllRows;
+    return p.slices > 1 && static_cast<int64_t>(p.batch) * (p.k + 1 + p.draft_rows) * p.vocab <= most;
 }
 
 size_t tree_bytes(const TreePlan& p) {

@@ -188,7 +188,7 @@ struct Next {
     double run, goal;
 };
 
-constexpr int kGroup = 16;  // bytes of registers / 2 that a group of tiles takes: 8 tiles of 16-bit, 4 of 32-bit elements
+constexpr int kGroup = 8;  // tiles whose loads are in flight together, times the size of an element (16 spilled, and was 9% slower)
 
 struct Shared {
     double wave_a[NWAVES], wave_b[NWAVES];
