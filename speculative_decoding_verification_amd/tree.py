@@ -21,7 +21,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 from . import (SV_BF16, SV_DRAFT_LOGITS, SV_DRAFT_ONEHOT, SVError, _check_dev, _dtype_code, _ptr, _stream_handle,
-               _torch, _Workspace, _workspace_bytes, load_library)
+               _torch, _workspace_bytes, load_library)
 
 __all__ = ["tree_attention", "TreeAttention", "verify_tree", "TreeVerifier", "cache_append", "cache_commit",
            "cache_fork", "cache_resize", "SV_F16"]
@@ -72,15 +72,39 @@ def bind(lib) -> None:
         f.restype, f.argtypes = res, args
 
 
-_WS_TREE = _Workspace()   # sv_verify_tree: zero-filled once, left ready by every call
-_WS_PLAIN = _Workspace()  # the others: needs no clearing
+class _Pool:
+    """Workspaces by (device, stream), grown on demand: calls on one stream run
+    in order and share one, calls on others may overlap.  An outgrown buffer is
+    kept, as work on a stream that torch does not know may still use it.
+    `zero`: the entry point wants its workspace zero-filled once."""
+
+    def __init__(self, zero: bool):
+        self._make = "zeros" if zero else "empty"
+        self._buf, self._old = {}, []
+
+    def new(self, device, nbytes: int):
+        torch = _torch()
+        return getattr(torch, self._make)(nbytes, dtype=torch.uint8, device=device)
+
+    def get(self, device, nbytes: int, stream: int):
+        buf = self._buf.get((device, stream))
+        if buf is None or buf.numel() < nbytes:
+            if buf is not None:
+                self._old.append(buf)
+            buf = self._buf[(device, stream)] = self.new(device, nbytes)
+            if self._make == "zeros" and stream != _stream_of(device, None):
+                _torch().cuda.current_stream(device).synchronize()  # the zeros are there before the other stream looks
+        return buf
 
 
-def _workspace(pool, device, nbytes: int, given=None, own: bool = False):
+_WS_TREE = _Pool(zero=True)    # sv_verify_tree: zero-filled once, left ready by every call
+_WS_PLAIN = _Pool(zero=False)  # the others: needs no clearing
+
+
+def _workspace(pool, device, nbytes: int, given=None, own: bool = False, stream: Optional[int] = None):
     """The caller's workspace, checked, or one of the pool's; a buffer of its own
     for a prepared call (`own`) and while a graph is captured, so that two graphs
     never share one."""
-    torch = _torch()
     if given is not None:
         if given.device != device or not given.is_contiguous():
             raise ValueError("workspace must be contiguous and on %s" % device)
@@ -89,9 +113,9 @@ def _workspace(pool, device, nbytes: int, given=None, own: bool = False):
         return given
     if device.type != "cuda" and not own:
         raise ValueError("tensors must be on a HIP device, got %s" % device)
-    if own or torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    return pool.get(device, nbytes)
+    if own or _torch().cuda.is_current_stream_capturing():
+        return pool.new(device, nbytes)
+    return pool.get(device, nbytes, _stream_of(device, stream))
 
 
 _HERE = contextlib.nullcontext()
@@ -197,7 +221,7 @@ class TreeAttention:
     may pass a common one."""
 
     def __init__(self, q, k_cache, v_cache, page_table, seq_len, parents=None, *, scale: Optional[float] = None,
-                 return_lse: bool = False, out=None, workspace=None, _pool=None):
+                 return_lse: bool = False, out=None, workspace=None, _pooled: bool = False):
         torch = _torch()
         lib = load_library()
         device = q.device
@@ -225,7 +249,7 @@ class TreeAttention:
                                       float(dim ** -0.5 if scale is None else scale), *strides)
         nbytes = _workspace_bytes(lib, lib.sv_tree_attention_workspace_bytes, lib.sv_tree_attention, self.desc,
                                   [None] * 9 + [0, None], "sv_tree_attention")
-        workspace = _workspace(_pool, device, nbytes, workspace, own=_pool is None)
+        workspace = _workspace(_WS_PLAIN, device, nbytes, workspace, own=not _pooled)
         if out is None:
             out = torch.empty((B, rows, heads, dim), dtype=q.dtype, device=device)
         else:
@@ -258,7 +282,7 @@ def tree_attention(q, k_cache, v_cache, page_table, seq_len, parents=None, *, sc
     contiguous of q's shape.
     """
     return TreeAttention(q, k_cache, v_cache, page_table, seq_len, parents, scale=scale, return_lse=return_lse,
-                         out=out, workspace=workspace, _pool=_WS_PLAIN)()
+                         out=out, workspace=workspace, _pooled=True)()
 
 
 class TreeVerifyOutput(NamedTuple):
@@ -272,7 +296,7 @@ class TreeVerifier:
     passed in must have been zero-filled once and serve sv_verify_tree alone."""
 
     def __init__(self, target, draft, draft_tokens, parents, uniforms, temperature: float, *, onehot: bool = False,
-                 workspace=None, _pool=None):
+                 workspace=None, _pooled: bool = False):
         torch = _torch()
         lib = load_library()
         if target.dim() != 3:
@@ -305,7 +329,7 @@ class TreeVerifier:
                                    float(temperature))
         nbytes = _workspace_bytes(lib, lib.sv_verify_tree_workspace_bytes, lib.sv_verify_tree, self.desc,
                                   [None] * 9 + [0, None], "sv_verify_tree")
-        workspace = _workspace(_pool, device, nbytes, workspace, own=_pool is None)
+        workspace = _workspace(_WS_TREE, device, nbytes, workspace, own=not _pooled)
         self.accepted_len = torch.empty(B, dtype=torch.int32, device=device)
         self.out_tokens = torch.empty((B, k + 1), dtype=torch.int32, device=device)
         self.path = torch.empty((B, k), dtype=torch.int32, device=device)
@@ -334,7 +358,7 @@ def verify_tree(target, draft, draft_tokens, parents, uniforms, temperature: flo
     Returns (accepted_len [B], out_tokens [B][k+1], path [B][k]).
     """
     return TreeVerifier(target, draft, draft_tokens, parents, uniforms, temperature, onehot=onehot,
-                        workspace=workspace, _pool=_WS_TREE)()
+                        workspace=workspace, _pooled=True)()
 
 
 def _append_plan(k_new, v_new, k_cache, v_cache, page_table, seq_len, count):
@@ -450,7 +474,7 @@ def cache_fork(src, dst, k_cache, v_cache, page_table, page_count, page_refs, se
         plan = _FORKS.keep(key, _fork_plan(lib, src, dst, k_cache, v_cache, page_table, page_count, page_refs,
                                            seq_len, status))
     desc, n, nbytes = plan
-    workspace = _workspace(_WS_PLAIN, device, nbytes, workspace)
+    workspace = _workspace(_WS_PLAIN, device, nbytes, workspace, stream=stream)
     with _on(device):
         st = lib.sv_cache_fork(ctypes.byref(desc), n, _ptr(src), _ptr(dst), _ptr(page_table), _ptr(page_count),
                                _ptr(page_refs), _ptr(seq_len), _ptr(k_cache), _ptr(v_cache), _ptr(status),

@@ -121,6 +121,7 @@ ATTENTION = [
     dict(k=16, hq=16, hkv=2, lens=(255, 600), page=128), dict(k=64, hq=8, hkv=1, lens=(40, 700), page=16),
     dict(k=64, hq=2, hkv=2, D=64, lens=(1, 2, 3), page=1), dict(k=64, hq=4, hkv=2, D=256, lens=(64, 65), page=1024),
     dict(k=8, hq=14, hkv=2, lens=(77, 1000, 5), absent=0.4), dict(k=64, hq=5, hkv=1, lens=(20,), absent=0.2),
+    dict(k=64, hq=256, hkv=1, D=64, lens=(50,)), dict(k=20, hq=256, hkv=2, D=256, lens=(9, 70)),
     dict(k=4, lens=(10, -1, 0, -5, 60), absent=0.3), dict(k=2, lens=(-1, -1)),
     dict(k=6, lens=(50, 90), amp=8.0), dict(k=6, lens=(50, 90), amp=8.0, dtype="f16", D=64),
     dict(k=6, lens=(50, 90), fill=float("inf")), dict(k=6, lens=(50, 90), scale=1e-3),
@@ -296,7 +297,7 @@ def check_walk(dev, t, d, tok, par, u, T, onehot):
     for b in range(len(tok)):
         a, o, p, margin = ref.walk(t64[b], None if d64 is None or onehot else d64[b], tok[b], par[b],
                                    u[b].astype(np.float64), T, onehot)
-        if margin < 1e-10:  # closer to a border than 64-bit sums tell apart
+        if margin <= 1.0:  # closer to a border than the kernel's sums tell apart
             continue
         assert (acc[b], list(out[b]), list(path[b])) == (a, o, p), "sequence %d" % b
         depth.append(a)
@@ -338,7 +339,7 @@ def test_walk_large_vocabulary(dev, onehot, B):
     ts, ds = t[some].double().cpu().numpy(), d[some].double().cpu().numpy()
     for i, b in enumerate(some):
         a, o, p, margin = ref.walk(ts[i], ds[i], tok[b], par[b], u[b].astype(np.float64), 1.0, onehot)
-        if margin >= 1e-10:
+        if margin > 1.0:
             assert (acc[b], list(out[b]), list(path[b])) == (a, o, p), "sequence %d" % b
 
 
@@ -359,10 +360,23 @@ def test_walk_on_a_chain_is_verify(dev):
         r = sv.verify_tree(on(t), on(d), on(tok), on(par), on(u), 1.0, onehot=onehot)
         for b in range(B):
             margin = ref.walk(t[b].double().numpy(), d[b].double().numpy(), tok[b], par[b], u[b].astype(np.float64), 1.0,
-                              onehot)[3]
-            if margin > 1e-5:
+                              onehot, e=1e-5)[3]
+            if margin > 1.0:
                 assert int(a.accepted_len[b]) == int(r.accepted_len[b])
                 assert torch.equal(a.out_tokens[b], r.out_tokens[b])
+
+
+@pytest.mark.parametrize("onehot", [False, True], ids=["logits", "onehot"])
+@pytest.mark.parametrize("T,amp,shift", [(1e-4, 1.0, 0.0), (0.05, 30.0, 0.0), (50.0, 300.0, -2e4), (1.0, 1.0, 1e6), (1.0, 200.0, 0.0)])
+def test_walk_extreme_temperatures_and_logits(dev, T, amp, shift, onehot):
+    """Rows that are one token, rows that are flat, and logits far from zero: l / T from 1e-2 to 1e6."""
+    t, d, tok, par, u = logits_case(8, 12, 10, 6000, 1.0, onehot, absent=0.0)
+    t, d = t * amp + shift, d * amp + shift
+    for b in range(12):
+        for i in range(10):
+            if (b + i) % 2:
+                tok[b, i] = int(t[b, par[b, i] + 1].argmax())
+    check_walk(dev, t, d, tok, par, u, T, onehot)
 
 
 def test_walk_refused_trees(dev):
@@ -611,6 +625,50 @@ def test_fork(dev, P_free):
     for a, b in ((dt, table), (dc, count), (dr, refs), (dl, lens)):
         assert np.array_equal(a.cpu().numpy(), b)
     assert same_bits(kd.cpu(), kc) and same_bits(vd.cpu(), vc)
+
+
+def test_cache_far_offsets(dev):
+    """Positions whose offset in the cache passes 2^32 elements: append, commit and fork against plain indexing."""
+    L, P, hkv, page, D = 2, 4200, 16, 256, 128  # 4.4e9 elements, the second layer's from 2.2e9 on
+    kc = torch.empty((L, P, hkv, page, D), dtype=torch.bfloat16, device=dev)
+    vc = torch.empty_like(kc)
+    table = torch.tensor([[4199, 4198], [-1, -1]], dtype=torch.int32, device=dev)
+    count = torch.tensor([2, 0], dtype=torch.int32, device=dev)
+    refs = torch.ones(P, dtype=torch.int32, device=dev)
+    refs[4197] = 0
+    lens = torch.tensor([250, 0], dtype=torch.int32, device=dev)
+    new = torch.randn((L, 2, 9, 2, hkv, D), device=dev).to(torch.bfloat16)
+    for l in range(L):
+        sv.cache_append(new[l, :, :, 0], new[l, :, :, 1], kc[l], vc[l], table, lens)
+    at = [(4199, 250 + j) if j < 6 else (4198, j - 6) for j in range(9)]
+    for j, (i, o) in enumerate(at):
+        assert torch.equal(kc[:, i, :, o], new[:, 0, j, 0]) and torch.equal(vc[:, i, :, o], new[:, 0, j, 1])
+    path = torch.tensor([[1, 4, 7, -1, -1, -1, -1, -1], [-1] * 8], dtype=torch.int32, device=dev)
+    acc = torch.tensor([3, -1], dtype=torch.int32, device=dev)
+    n = sv.cache_commit(path, acc, kc, vc, table, lens)
+    assert n.tolist() == [254, 0]
+    for j, src in enumerate((1, 4, 7)):
+        i, o = at[1 + j]
+        assert torch.equal(kc[:, i, :, o], new[:, 0, 1 + src, 0]) and torch.equal(vc[:, i, :, o], new[:, 0, 1 + src, 1])
+    ok = sv.cache_fork(torch.zeros(1, dtype=torch.int32, device=dev), torch.ones(1, dtype=torch.int32, device=dev), kc, vc,
+                       table, count, refs, n)
+    assert ok.tolist() == [1] and table.tolist() == [[4199, 4198], [4197, -1]]
+    assert torch.equal(kc[:, 4197, :, 250:254], kc[:, 4199, :, 250:254]) and torch.equal(vc[1, 4197, 3, 253], vc[1, 4199, 3, 253])
+
+
+def test_empty_batches(dev):
+    z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device=dev)  # noqa: E731
+    c = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device=dev)
+    out = sv.tree_attention(z(0, 4, 8, 64, t=torch.bfloat16), c, c.clone(), z(0, 3), z(0), z(0, 3), return_lse=True)
+    assert out.out.shape == (0, 4, 8, 64) and out.lse.shape == (0, 4, 8)
+    r = sv.verify_tree(z(0, 4, 10, t=torch.float32), None, z(0, 3), z(0, 3), None, 0.0)
+    assert r.path.shape == (0, 3)
+    sv.cache_append(z(0, 4, 2, 64, t=torch.bfloat16), z(0, 4, 2, 64, t=torch.bfloat16), c, c.clone(), z(0, 3), z(0))
+    sv.cache_append(z(2, 0, 2, 64, t=torch.bfloat16), z(2, 0, 2, 64, t=torch.bfloat16), c, c.clone(), z(2, 3), z(2))
+    k5 = c[None].contiguous()
+    assert sv.cache_commit(z(0, 3), z(0), k5, k5.clone(), z(0, 3), z(0)).shape == (0,)
+    assert sv.cache_fork(z(0), z(0), k5, k5.clone(), z(2, 3), z(2), z(4), z(2)).shape == (0,)
+    assert sv.cache_resize(z(0), z(0, 3), z(0), z(4), page_size=16).shape == (0,)
 
 
 # ------------------------------------------------------------------------------------------- a run of them together

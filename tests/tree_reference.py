@@ -49,9 +49,19 @@ def attention(q, kc, vc, table, lens, parents, scale):
     return out, lse, absv, dot
 
 
-def walk(target, draft, tokens, parents, u, T, onehot):
-    """One sequence: (accepted_len, out_tokens [k+1], path [k], margin), margin the least distance of a test or of the
-    draw from its border (relative to the mass it is taken from).  target [k+1][V], draft [R][V] or None, float64."""
+# Relative error of a probability that sv_verify_tree forms: its 2^f is good to 5.6e-11 (a polynomial of degree 7), a sum
+# of such terms is no worse, and a probability is one over the other: 1.12e-10, and the roundings of 64 bits (1e-14).
+KERNEL_ERROR = 1.2e-10
+
+
+def walk(target, draft, tokens, parents, u, T, onehot, e=KERNEL_ERROR):
+    """One sequence: (accepted_len, out_tokens [k+1], path [k], margin).  target [k+1][V], draft [R][V] or None, float64.
+
+    margin: the least distance of a test or of the draw from its border, over what a computation whose probabilities
+    have the relative error `e` can be off there; above 1 the result is settled.  `off` bounds the residual's error token
+    by token: e r at first; max(0, r - q) is off by at most off + e q, or by nothing where q is larger beyond that, and its
+    division by the sum F by another sum(off) / F of itself, so that a residual of two nearly equal rows (a small F) is
+    known less well."""
     k, V = len(tokens), target.shape[1]
     bad = False
     R = 0 if draft is None else draft.shape[0]
@@ -63,8 +73,8 @@ def walk(target, draft, tokens, parents, u, T, onehot):
         if 0 <= p < i:
             bad |= parents[p] == -2 or (not onehot and T != 0 and p + 1 >= R)
     if bad:
-        return -1, [-1] * (k + 1), [-1] * k, 1.0
-    at, path, margin = -1, [], 1.0
+        return -1, [-1] * (k + 1), [-1] * k, np.inf
+    at, path, margin = -1, [], np.inf
     while True:
         kids = [i for i in range(k) if parents[i] == at]
         row = target[at + 1]
@@ -75,6 +85,7 @@ def walk(target, draft, tokens, parents, u, T, onehot):
         else:
             r = np.exp((row - row.max()) / T)
             r /= r.sum()
+            off = e * r
             q = None
             if kids and not onehot:
                 d = draft[at + 1]
@@ -83,21 +94,24 @@ def walk(target, draft, tokens, parents, u, T, onehot):
             for i in kids:
                 x = tokens[i]
                 a, c = u[i] * (1.0 if q is None else q[x]), r[x]
-                margin = min(margin, abs(a - c) / max(a, c, 1e-300))
+                margin = min(margin, abs(a - c) / max(2 * e * a + off[x], 1e-300))
                 if a < c:
                     hit = i
                     break
                 if q is None:
-                    r = r.copy()
-                    r[x] = 0.0
+                    r, off = r.copy(), off.copy()
+                    r[x] = off[x] = 0.0
                 else:
-                    r = np.maximum(0.0, r - q)
-                r = r / r.sum()
+                    r, off = np.maximum(0.0, r - q), np.where(r + off < q - e * q, 0.0, off + e * q)
+                F, off_F = r.sum(), off.sum()
+                if F <= off_F:
+                    return None, None, None, 0.0  # nothing is known of what is left
+                r, off = r / F, (off + r * (off_F / F)) / F
             if hit is None:
                 C = np.cumsum(r)
                 goal = u[k] * C[-1]
                 y = min(V - 1, int(np.searchsorted(C, goal, side="right")))
-                margin = min(margin, float(np.abs(C - goal).min()) / C[-1])
+                margin = min(margin, float((np.abs(C - goal) / (np.cumsum(off) + u[k] * off.sum() + 1e-14)).min()))
         if hit is None:
             toks = [int(tokens[i]) for i in path] + [y]
             return len(path), toks + [-1] * (k + 1 - len(toks)), path + [-1] * (k - len(path)), margin
