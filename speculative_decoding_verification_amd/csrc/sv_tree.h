@@ -64,11 +64,11 @@ hipError_t launch_tree_attention(const AttnPlan& p, hipStream_t stream);
 
 // ---- verification of a tree ---------------------------------------------------
 
-constexpr int kTreeThreads = 512;
+constexpr int kTreeThreads = 256;
 constexpr int kTreeMaxSlices = 64;
 constexpr int kTreeMaxBatch = 65535;
-constexpr int kTreeWgs = 512;    // workgroups of a walk's pass: as many as run at once
-constexpr int kTreeRowWgs = 1024;  // workgroups that read every row at once, about
+constexpr int kTreeWgs = 1024;    // workgroups of a walk's pass: as many as run at once
+constexpr int kTreeRowWgs = 2048;  // workgroups that read every row at once, about
 constexpr int kTreeDies = 8;
 constexpr uint64_t kTreeWaitTicks = 2000000;  // of 10 ns: how long a workgroup waits for the others of its sequence
 constexpr int kTreeTile = kTreeThreads * 8;  // tokens one workgroup takes at a time

@@ -19,9 +19,8 @@
 //
 // Arithmetic is 64-bit: with 10^5 tokens of similar mass a relative error of
 // 1e-7 in a cumulative sum moves about one draw in a hundred to another token.
-// 2^f is a polynomial of degree 7 (Chebyshev nodes on [-1/2, 1/2], relative
-// error 4e-11, one draw in 10^5 at worst).  64-bit multiply-adds run at the
-// rate of 32-bit ones here (5.3 against 4.7 cycles a wavefront, measured).
+// 2^x is good to 4.5e-12 (Power).  64-bit multiply-adds run at about the rate of
+// 32-bit ones here (5.3 against 4.7 cycles a wavefront, measured).
 // Row maxima are kept as whole powers of two (M >= max l c2), so that sums over
 // parts of a row join by exact shifts, and the rounding to the power, the
 // exponent's bias and M are one constant: see Power.
@@ -47,30 +46,42 @@ enum TreeStage : int32_t {
     kStageDone = 2
 };
 
-// 2^(l c2 - M) for logits l.  k1 = 1.5 2^52 + 1023 - M: the sum l c2 + k1 is
-// rounded to a whole number, whose low word is the biased exponent of the
-// result; what the rounding took off is the polynomial's argument.  Logits are
-// raised to `low`, where the result is 2^-1000: nothing in a sum, and the
-// exponent stays in range (a logit of -inf counts as that, see zero_mass).
+// 2^(l c2 - M) for logits l.  k1 = 1.5 2^46 + 1023 - M: the sum l c2 + k1 is
+// rounded to a multiple of 1/64, whose low word is 64 times the biased exponent
+// plus the index i of 2^(i / 64) in the table; what the rounding took off, at
+// most 1/128, is the polynomial's argument (degree 3 at Chebyshev nodes,
+// relative error 4.5e-12).  The table's high words have i 2^14 taken off, so
+// that the low word, shifted by 14, adds the exponent and nothing else.  64
+// entries are two to each pair of LDS banks: a read takes two turns at most.
+// Against one polynomial of degree 7 (5.5e-11, 14 operations of 64 bits a
+// logit) this is 9 of 64 bits and three of 32.  Logits are raised to `low`,
+// where the result is 2^-1000: nothing in a sum, and the exponent stays in
+// range (a logit of -inf is never drawn, see slice_draw).
+constexpr int kPow2 = 64;
+
+__device__ __forceinline__ double pow2_entry(int i) {
+    const double t = exp2(static_cast<double>(i) / kPow2);
+    return __hiloint2double((__double2hiint(t) & 0xFFFFF) - (i << 14), __double2loint(t));
+}
+
 struct Power {
+    const double* table;
     double c2, k1, low;
-    __device__ __forceinline__ Power(double c2_, double m) : c2(c2_) {
-        k1 = 6755399441055744.0 + (1023.0 - m);
+    __device__ __forceinline__ Power(const double* table_, double c2_, double m) : table(table_), c2(c2_) {
+        k1 = 105553116266496.0 + (1023.0 - m);
         low = (m - 1000.0) / c2_;
     }
     __device__ __forceinline__ double operator()(float l) const {
         const double x = __builtin_fmax(static_cast<double>(l), low);
         const double s = __builtin_fma(x, c2, k1);
         const double f = __builtin_fma(x, c2, k1 - s);
-        double r = 1.5303700711425663e-05;
-        r = __builtin_fma(r, f, 0.00015469729214122798);
-        r = __builtin_fma(r, f, 0.0013333478473685175);
-        r = __builtin_fma(r, f, 0.009618025613318018);
-        r = __builtin_fma(r, f, 0.055504109063258665);
-        r = __builtin_fma(r, f, 0.24022651213498092);
-        r = __builtin_fma(r, f, 0.6931471805568324);
-        r = __builtin_fma(r, f, 0.9999999999595618);
-        return r * __hiloint2double(__double2loint(s) << 20, 0);
+        const int n = __double2loint(s);
+        const double t = table[n & (kPow2 - 1)];
+        double r = 0.055504190037736274;
+        r = __builtin_fma(r, f, 0.24022709400357053);
+        r = __builtin_fma(r, f, 0.6931471805593249);
+        r = __builtin_fma(r, f, 0.9999999999955212);
+        return r * __hiloint2double(__double2hiint(t) + static_cast<int>(static_cast<uint32_t>(n) << 14), __double2loint(t));
     }
 };
 
@@ -191,6 +202,7 @@ struct Next {
 constexpr int kGroup = 8;  // tiles whose loads are in flight together, times the size of an element (16 spilled, and was 9% slower)
 
 struct Shared {
+    double pow2[kPow2];
     double wave_a[NWAVES], wave_b[NWAVES];
     float wave_f[NWAVES];
     int wave_i[NWAVES];
@@ -292,7 +304,7 @@ __device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, doub
             z = was == -__builtin_inff() ? 0.0 : shift_to(z, m, mn);
             m = mn;
         }
-        const Power power(c2, m);
+        const Power power(sh.pow2, c2, m);
 #pragma unroll
         for (int t = 0; t < GROUP; ++t) {
             if (base + t * (NT * kPer) >= hi) continue;  // the whole workgroup at once
@@ -312,8 +324,8 @@ __device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, doub
 struct Mass {
     Power p, q;
     double iz, tq;
-    __device__ __forceinline__ Mass(const TreeState& s, double c2)
-        : p(c2, s.m_t), q(c2, s.m_q), iz(1.0 / s.z_t), tq(s.t / s.z_q) {}
+    __device__ __forceinline__ Mass(const double* pow2, const TreeState& s, double c2)
+        : p(pow2, c2, s.m_t), q(pow2, c2, s.m_q), iz(1.0 / s.z_t), tq(s.t / s.z_q) {}
     __device__ __forceinline__ double operator()(float lt, float lq) const {
         return __builtin_fmax(0.0, __builtin_fma(-tq, q(lq), iz * p(lt)));
     }
@@ -324,7 +336,7 @@ template <typename T>
 __device__ double slice_mass(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, double c2, const TreeState& s,
                              Shared& sh) {
     constexpr int GROUP = kGroup / sizeof(T) / 2;
-    const Mass mass(s, c2);
+    const Mass mass(sh.pow2, s, c2);
     double f = 0.0;
     for (int64_t base = lo; base < hi; base += GROUP * NT * kPer) {
         Raw<T> a[GROUP], b[GROUP];
@@ -353,7 +365,7 @@ template <typename T>
 __device__ int slice_draw(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, double c2, const TreeState& s,
                           double run, double goal, Shared& sh) {
     const bool pair = qr != nullptr;
-    const Mass mass(s, c2);
+    const Mass mass(sh.pow2, s, c2);
     int last = static_cast<int>(lo);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t base = lo; base < hi; base += NT * kPer) {
@@ -422,13 +434,14 @@ struct Node {
     int up, tok;
     double u;
     float l, d;  // the logits of its token in its parent's target and draft row
+    int kept;    // not of node i: the i-th node that this workgroup saw kept, or -1
 };
 
 template <typename T, int KIND>
 __device__ __forceinline__ Node node_of(const TreePlan& p, int b) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
-    Node n{-2, -1, 0.0, 0.f, 0.f};
+    Node n{-2, -1, 0.0, 0.f, 0.f, -1};
     if (lane < p.k) {
         n.up = p.parents[bk + lane];
         n.tok = p.tokens[bk + lane];
@@ -450,9 +463,10 @@ __device__ __forceinline__ Node node_of(const TreePlan& p, int b) {
 // The walk's next decision, taken by the first wavefront.  On entry st holds
 // the row's statistics (or F(t)); on return its stage says what is needed next,
 // and the answer is true when a token is to be drawn from what is left at st.at.
-// Every workgroup of a sequence may take the decision, one (`lead`) writes it.
+// Every workgroup of a sequence may take the decision, one (`lead`) writes it as
+// it is taken; the one that draws writes it again, for `lead` may have left.
 template <int KIND>
-__device__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
+__device__ bool decide(const TreePlan& p, int b, Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
     const bool child = (st.left >> lane) & 1;
@@ -464,10 +478,10 @@ __device__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st
     } else {
         double px = 0.0, qx = 0.0;
         if (child) {
-            const Power pt(p.c2, st.m_t);
+            const Power pt(sh.pow2, p.c2, st.m_t);
             px = node.l < pt.low ? 0.0 : pt(node.l) / st.z_t;
             if (KIND == kTreeLogits) {
-                const Power pq(p.c2, st.m_q);
+                const Power pq(sh.pow2, p.c2, st.m_q);
                 qx = node.d < pq.low ? 0.0 : pq(node.d) / st.z_q;
             }
         }
@@ -512,6 +526,7 @@ __device__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st
             p.path[bk + st.kept] = hit;
             p.out_tokens[bk + b + st.kept] = x;
         }
+        if (lane == st.kept) node.kept = hit;
         st.kept += 1;
         st.at = hit;
         st.left = __ballot(node.up == hit);
@@ -553,9 +568,14 @@ __device__ void refuse(const TreePlan& p, int b) {
     }
 }
 
-__device__ void finish(const TreePlan& p, int b, const TreeState& st, int token) {
+__device__ void finish(const TreePlan& p, int b, const Node& node, const TreeState& st, int token) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
+    const int x = __shfl(node.tok, max(node.kept, 0));
+    if (node.kept >= 0 && lane < st.kept) {
+        p.path[bk + lane] = node.kept;
+        p.out_tokens[bk + b + lane] = x;
+    }
     if (lane == 0) {
         p.accepted_len[b] = st.kept;
         p.out_tokens[bk + b + st.kept] = token;
@@ -626,7 +646,7 @@ __device__ __forceinline__ bool fits(const TreePlan& p, int b, const Node& node,
 // p.row_part the statistics of every row are there already, and only a
 // residual's mass needs another pass.  st is what the next pass works on.
 template <typename T, int KIND>
-__device__ Next go_on(const TreePlan& p, int b, const Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
+__device__ Next go_on(const TreePlan& p, int b, Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
     const bool by_rows = p.row_part && st.stage == kStageRow;
     int slices = by_rows ? p.row_slices : p.slices;
@@ -689,14 +709,14 @@ __device__ Next go_on(const TreePlan& p, int b, const Node& node, TreeState& st,
 
 // The token that is due, and the sequence's end (the whole workgroup).
 template <typename T, int KIND>
-__device__ void draw_token(const TreePlan& p, int b, const TreeState& st, const Next& nx, Shared& sh) {
+__device__ void draw_token(const TreePlan& p, int b, const Node& node, const TreeState& st, const Next& nx, Shared& sh) {
     int y = nx.best;
     if (KIND != kTreeGreedy) {
         const Rows<T, KIND> rows(p, b, st);
         y = slice_draw(rows.target, st.stage == kStageMass ? rows.draft : static_cast<const T*>(nullptr), nx.from,
                        min(static_cast<int64_t>(p.vocab), nx.from + nx.len), p.vec != 0, p.c2, st, nx.run, nx.goal, sh);
     }
-    if (threadIdx.x < 64) finish(p, b, st, y);
+    if (threadIdx.x < 64) finish(p, b, node, st, y);
 }
 
 // The statistics of every row of the tree at once; the last workgroup of a
@@ -714,6 +734,7 @@ __global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
         const int up = tid < p.k ? p.parents[static_cast<int64_t>(b) * p.k + tid] : -2;
         const bool wanted = at < 0 || __shfl(up, max(at, 0)) != -2;
         const bool used = target || __ballot(up == at) != 0;
+        if (KIND != kTreeGreedy) sh.pow2[tid] = pow2_entry(tid);
         if (tid == 0) {
             sh.ibcast[0] = wanted && used;
             sh.n_gone = 0;
@@ -756,7 +777,7 @@ __global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
     __syncthreads();
     st = sh.st;
     const Next nx = sh.nx;
-    if (nx.draw) draw_token<T, KIND>(p, b, st, nx, sh);
+    if (nx.draw) draw_token<T, KIND>(p, b, node, st, nx, sh);
     if (tid == 0) {
         p.arrived[b] = 0;
         if (KIND == kTreeLogits) {  // the kernels that follow go on with it
@@ -802,6 +823,7 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
     }
     Node node{};
     if (tid < 64) {
+        if (KIND != kTreeGreedy) sh.pow2[tid] = pow2_entry(tid);
         node = node_of<T, KIND>(p, b);
         if (first) {
             begin<KIND>(p, b, node, st);
@@ -896,7 +918,7 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
             const bool mine = KIND == kTreeGreedy ? lead : slice == nx.from / p.per;
             if (mine) {
                 st = sh.st;
-                draw_token<T, KIND>(p, b, st, nx, sh);
+                draw_token<T, KIND>(p, b, node, st, nx, sh);
                 if (tid == 0) p.finished[b] = 1;
             }
             return;
@@ -921,6 +943,7 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
         if (done) return;
     }
     if (threadIdx.x < 64) {
+        if (KIND != kTreeGreedy) sh.pow2[threadIdx.x] = pow2_entry(threadIdx.x);
         TreeState st{};
         if (!first) st = p.state[b];
         const bool ranged = first || in_range<KIND>(p, st);
@@ -966,7 +989,7 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
             y = slice_draw(rows.target, st.stage == kStageMass ? rows.draft : static_cast<const T*>(nullptr), 0, V, vec,
                            p.c2, st, 0.0, u * all, sh);
         }
-        if (threadIdx.x < 64) finish(p, b, st, y);
+        if (threadIdx.x < 64) finish(p, b, node, st, y);
         return;
     }
 }

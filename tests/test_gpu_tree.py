@@ -492,6 +492,28 @@ def test_walk_when_no_workgroup_waits(dev, onehot, T):
         assert all(torch.equal(x, y) for x, y in zip(sv.verify_tree(*a, T, onehot=onehot), w))
 
 
+@pytest.mark.parametrize("onehot", [False, True], ids=["logits", "onehot"])
+def test_walk_when_some_workgroups_leave(dev, onehot):
+    """Waits of about as long as a pass takes: a workgroup may leave, the first one too, in a pass in which the others
+    see a node kept and the token drawn."""
+    import ctypes
+
+    lib = sv.load_library()
+    lib.sv_internal_tree_wait.argtypes = [ctypes.c_uint64]
+    cases = [logits_case(B, B, k, V, 1.0, onehot) for B, k, V in ((90, 6, 20000), (100, 5, 20000), (60, 16, 50000))]
+    on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
+    args = [tuple(on(x) for x in c) for c in cases]
+    want = [[x.clone() for x in sv.verify_tree(*a, 1.0, onehot=onehot)] for a in args]
+    try:
+        for ticks in (30, 60, 100, 150, 220, 300, 500) * 3:
+            lib.sv_internal_tree_wait(ticks)
+            for i, (a, w) in enumerate(zip(args, want)):
+                got = sv.verify_tree(*a, 1.0, onehot=onehot)
+                assert all(torch.equal(x, y) for x, y in zip(got, w)), (ticks, i)
+    finally:
+        lib.sv_internal_tree_wait(2000000)
+
+
 def test_walks_on_two_streams_at_once(dev):
     on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
     cases = [tuple(on(x) for x in logits_case(i, 120, 8, 40000, 1.0, False)) for i in range(2)]

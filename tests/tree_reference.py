@@ -49,9 +49,9 @@ def attention(q, kc, vc, table, lens, parents, scale):
     return out, lse, absv, dot
 
 
-# Relative error of a probability that sv_verify_tree forms: its 2^f is good to 5.6e-11 (a polynomial of degree 7), a sum
-# of such terms is no worse, and a probability is one over the other: 1.12e-10, and the roundings of 64 bits (1e-14).
-KERNEL_ERROR = 1.2e-10
+# Relative error of a probability that sv_verify_tree forms: its 2^f is good to 4.5e-12 (a table and a polynomial), a sum
+# of such terms is no worse, and a probability is one over the other: 9e-12, and the roundings of 64 bits (1e-14).
+KERNEL_ERROR = 1e-11
 
 
 def walk(target, draft, tokens, parents, u, T, onehot, e=KERNEL_ERROR):
