@@ -67,8 +67,13 @@ hipError_t launch_tree_attention(const AttnPlan& p, hipStream_t stream);
 constexpr int kTreeThreads = 256;
 constexpr int kTreeMaxSlices = 64;
 constexpr int kTreeMaxBatch = 65535;
-constexpr int kTreeWgs = 1024;    // workgroups of a walk's pass: as many as run at once
-constexpr int kTreeRowWgs = 2048;  // workgroups that read every row at once, about
+constexpr int kTreeWgs = 1024;   // workgroups of a walk's pass: as many as run at once
+// Workgroups that read every row at once, about: what runs at once, and twice
+// that where draft rows are among them, of which those of leaves are not read.
+// 8 x 17 rows of 151936: 39 us with 1024, 42 with 1536, 44 with 2048; with a
+// drafter's rows 89, 79 and 72.
+constexpr int kTreeRowWgs = 1024;
+constexpr int kTreeRowWgsLogits = 2048;
 constexpr int kTreeDies = 8;
 constexpr uint64_t kTreeWaitTicks = 2000000;  // of 10 ns: how long a workgroup waits for the others of its sequence
 constexpr int kTreeTile = kTreeThreads * 8;  // tokens one workgroup takes at a time

@@ -105,8 +105,8 @@ sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     p->elem_bytes = d->dtype == SV_BF16 ? 2 : 4;
     p->c2 = t == 0.f ? 0.0 : kLog2E / static_cast<double>(t);
     tree_slices(p->vocab, p->batch, kTreeWgs, &p->per, &p->slices);
-    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows), kTreeRowWgs, &p->row_per,
-                &p->row_slices);
+    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows),
+                p->kind == kTreeLogits ? kTreeRowWgsLogits : kTreeRowWgs, &p->row_per, &p->row_slices);
     p->wait_ticks = tree_wait_ticks;
     return SV_OK;
 }

@@ -211,6 +211,7 @@ struct Shared {
     int gone[SV_MAX_DRAFT];  // one-hot: the rejected siblings' tokens and their p
     double gone_p[SV_MAX_DRAFT];
     int n_gone;
+    double row_m[2 * SV_MAX_DRAFT + 2], row_z[2 * SV_MAX_DRAFT + 2];  // every row's statistics: join_rows
     TreeState st;
     Next nx;
 };
@@ -641,6 +642,45 @@ __device__ __forceinline__ bool fits(const TreePlan& p, int b, const Node& node,
     return start.stage != kStageDone && (st.left & ~__ballot(node.up == st.at)) == 0;
 }
 
+// Joins the partials of every row, those that were read at once, for the first
+// wavefront, by the others: several rows to a wavefront, a lane to a slice.
+template <int KIND>
+__device__ __forceinline__ void join_rows(const TreePlan& p, int b, Shared& sh) {
+    const int rows = p.k + 1 + p.draft_rows;
+    int width = 1;
+    while (width < p.row_slices) width <<= 1;
+    const int i = threadIdx.x & (width - 1);
+    for (int row = (threadIdx.x - 64) / width; row < rows; row += (NT - 64) / width) {
+        const double* const part = p.row_part + ((static_cast<int64_t>(b) * rows + row) * kTreeMaxSlices + i) * 2;
+        double m = 0.0, z = 0.0;
+        if (i < p.row_slices) {
+            m = taken(part);
+            z = taken(part + 1);
+        }
+        if (KIND == kTreeGreedy) {  // (maximum, lowest index)
+            if (i >= p.row_slices) m = -__builtin_inf(), z = INT_MAX;
+            for (int d = width >> 1; d; d >>= 1) {
+                const double om = __shfl_xor(m, d), oz = __shfl_xor(z, d);
+                if (om > m || (om == m && oz < z)) {
+                    m = om;
+                    z = oz;
+                }
+            }
+            if (i == 0) sh.row_z[row] = z;
+            continue;
+        }
+        double top = z > 0.0 ? m : -1e300;
+        for (int d = width >> 1; d; d >>= 1) top = __builtin_fmax(top, __shfl_xor(top, d));
+        if (top == -1e300) top = 0.0;
+        double sum = z > 0.0 ? shift_to(z, m, top) : 0.0;
+        for (int d = width >> 1; d; d >>= 1) sum += __shfl_xor(sum, d);
+        if (i == 0) {
+            sh.row_m[row] = top;
+            sh.row_z[row] = sum;
+        }
+    }
+}
+
 // Goes on with a walk whose pass is complete, as far as what is known reaches
 // (the first wavefront).  r: the pass's partials, lane i's of slice i.  With
 // p.row_part the statistics of every row are there already, and only a
@@ -648,32 +688,29 @@ __device__ __forceinline__ bool fits(const TreePlan& p, int b, const Node& node,
 template <typename T, int KIND>
 __device__ Next go_on(const TreePlan& p, int b, Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
-    const bool by_rows = p.row_part && st.stage == kStageRow;
-    int slices = by_rows ? p.row_slices : p.slices;
-    int64_t per = by_rows ? p.row_per : p.per;
+    int slices = p.slices;
+    int64_t per = p.per;
     Next nx{false, 0, 0, 0, 0.0, 0.0};
     double mass = 0.0;  // of this lane's slice
     while (true) {
-        if (p.row_part && st.stage == kStageRow) {
+        const bool by_rows = p.row_part && st.stage == kStageRow;
+        if (by_rows) {
             slices = p.row_slices;
             per = p.row_per;
-            const int rows = p.k + 1 + p.draft_rows;
-            const double* const at = p.row_part + (static_cast<int64_t>(b) * rows * kTreeMaxSlices + lane) * 2;
-            const int64_t tr = static_cast<int64_t>(st.at + 1) * kTreeMaxSlices * 2;
-            const int64_t dr = static_cast<int64_t>(p.k + 1 + st.at + 1) * kTreeMaxSlices * 2;
-            if (lane < slices) {
-                r[0] = taken(at + tr);
-                r[1] = taken(at + tr + 1);
-                if (KIND == kTreeLogits && st.left) {
-                    r[2] = taken(at + dr);
-                    r[3] = taken(at + dr + 1);
-                }
-            }
         }
-        if (KIND == kTreeGreedy) {
+        if (KIND == kTreeGreedy && by_rows) {
+            nx.best = static_cast<int>(sh.row_z[st.at + 1]);
+        } else if (KIND == kTreeGreedy) {
             float m = lane < slices ? static_cast<float>(r[0]) : -__builtin_inff();
             nx.best = lane < slices ? static_cast<int>(r[1]) : INT_MAX;
             wave_argmax(m, nx.best);
+        } else if (by_rows) {
+            st.m_t = sh.row_m[st.at + 1];
+            st.z_t = sh.row_z[st.at + 1];
+            if (KIND == kTreeLogits && st.left) {
+                st.m_q = sh.row_m[p.k + 1 + st.at + 1];
+                st.z_q = sh.row_z[p.k + 1 + st.at + 1];
+            }
         } else if (st.stage == kStageRow) {
             mass = join(lane < slices, r[0], r[1], &st.m_t, &st.z_t) / st.z_t;
             if (KIND == kTreeLogits && st.left) join(lane < slices, r[2], r[3], &st.m_q, &st.z_q);
@@ -685,6 +722,15 @@ __device__ Next go_on(const TreePlan& p, int b, Node& node, TreeState& st, doubl
         if (nx.draw || !p.row_part || st.stage != kStageRow) break;
     }
     if (nx.draw && KIND != kTreeGreedy) {
+        if (p.row_part && st.stage == kStageRow) {
+            const int64_t row = static_cast<int64_t>(b) * (p.k + 1 + p.draft_rows) + st.at + 1;
+            const double* const part = p.row_part + (row * kTreeMaxSlices + lane) * 2;
+            if (lane < slices) {
+                r[0] = taken(part);
+                r[1] = taken(part + 1);
+            }
+            mass = lane < slices && r[1] > 0.0 ? shift_to(r[1], r[0], st.m_t) / st.z_t : 0.0;
+        }
         if (KIND == kTreeOneHot) mass = __builtin_fmax(0.0, mass - gone_mass(sh, lane * per, (lane + 1) * per));
         if (lane >= slices) mass = 0.0;
         double cum = mass;
@@ -763,8 +809,10 @@ __global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
     if (!sh.ibcast[2]) return;
     Node node{};
     TreeState st{};
+    if (tid < 64) node = node_of<T, KIND>(p, b);
+    else join_rows<KIND>(p, b, sh);
+    __syncthreads();
     if (tid < 64) {
-        node = node_of<T, KIND>(p, b);
         begin<KIND>(p, b, node, st);
         Next nx{false, 0, 0, 0, 0.0, 0.0};
         if (st.stage == kStageDone) refuse(p, b);
@@ -838,6 +886,8 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
             sh.st = st;
             sh.n_gone = 0;
         }
+    } else if (p.row_part) {
+        join_rows<KIND>(p, b, sh);
     }
     const int64_t V = p.vocab, lo = slice * p.per, hi = min(V, lo + p.per);
     const bool vec = p.vec != 0;
