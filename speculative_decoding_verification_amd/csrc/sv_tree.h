@@ -120,7 +120,7 @@ struct TreePlan {
     int32_t elem_bytes;          // 4 fp32, 2 bf16
     int32_t vec;                 // rows start on 16-byte boundaries
     uint64_t wait_ticks;
-    double c2;                   // log2(e) / T
+    double c2, per_c2;           // log2(e) / T and one over it (0 and 0 for greedy walks)
 };
 
 hipError_t launch_verify_tree(const TreePlan& p, hipStream_t stream);

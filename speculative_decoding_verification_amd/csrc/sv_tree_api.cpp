@@ -104,6 +104,7 @@ sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     p->draft_rows = p->kind == kTreeLogits ? d->draft_rows : 0;
     p->elem_bytes = d->dtype == SV_BF16 ? 2 : 4;
     p->c2 = t == 0.f ? 0.0 : kLog2E / static_cast<double>(t);
+    p->per_c2 = t == 0.f ? 0.0 : static_cast<double>(t) / kLog2E;
     tree_slices(p->vocab, p->batch, kTreeWgs, &p->per, &p->slices);
     tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows),
                 p->kind == kTreeLogits ? kTreeRowWgsLogits : kTreeRowWgs, &p->row_per, &p->row_slices);

@@ -30,6 +30,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "specverify.h"
 #include "sv_tree.h"
@@ -64,12 +65,17 @@ __device__ __forceinline__ double pow2_entry(int i) {
     return __hiloint2double((__double2hiint(t) & 0xFFFFF) - (i << 14), __double2loint(t));
 }
 
+struct Scale {
+    double c2, per_c2;  // log2(e) / T and one over it
+    __device__ __forceinline__ explicit Scale(const TreePlan& p) : c2(p.c2), per_c2(p.per_c2) {}
+};
+
 struct Power {
     const double* table;
     double c2, k1, low;
-    __device__ __forceinline__ Power(const double* table_, double c2_, double m) : table(table_), c2(c2_) {
+    __device__ __forceinline__ Power(const double* table_, const Scale& c, double m) : table(table_), c2(c.c2) {
         k1 = 105553116266496.0 + (1023.0 - m);
-        low = (m - 1000.0) / c2_;
+        low = (m - 1000.0) * c.per_c2;
     }
     __device__ __forceinline__ double operator()(float l) const {
         const double x = __builtin_fmax(static_cast<double>(l), low);
@@ -154,27 +160,55 @@ __device__ __forceinline__ Raw<T> load8(const T* row, int64_t i, int64_t end, bo
     return r;
 }
 
+// The value of the lane that is D away, or for 4 and 8 of one in the
+// neighbouring group of as many: the same for a reduction, which has made the
+// lanes of a group alike by then.  Up to 8 it is an operand's permutation
+// (DPP), not a trip through LDS.
+template <int D>
+__device__ __forceinline__ int from_lane(int v) {
+    if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);       // 1 0 3 2 in four
+    else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);  // 2 3 0 1
+    else if constexpr (D == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true); // eight mirrored
+    else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true); // sixteen mirrored
+    else return __shfl_xor(v, D);
+}
+template <int D>
+__device__ __forceinline__ float from_lane(float v) {
+    return __int_as_float(from_lane<D>(__float_as_int(v)));
+}
+template <int D>
+__device__ __forceinline__ double from_lane(double v) {
+    return __hiloint2double(from_lane<D>(__double2hiint(v)), from_lane<D>(__double2loint(v)));
+}
+
+template <typename F>
+__device__ __forceinline__ void reduce_steps(const F& f) {
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 4>{});
+    f(std::integral_constant<int, 8>{});
+    f(std::integral_constant<int, 16>{});
+    f(std::integral_constant<int, 32>{});
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    reduce_steps([&](auto d) { v += from_lane<d.value>(v); });
     return v;
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    reduce_steps([&](auto d) { v = fmaxf(v, from_lane<d.value>(v)); });
     return v;
 }
 
 __device__ __forceinline__ void wave_argmax(float& m, int& at) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const float om = __shfl_xor(m, d);
-        const int oa = __shfl_xor(at, d);
+    reduce_steps([&](auto d) {
+        const float om = from_lane<d.value>(m);
+        const int oa = from_lane<d.value>(at);
         if (om > m || (om == m && oa < at)) {
             m = om;
             at = oa;
         }
-    }
+    });
 }
 
 // Joins the (M, sum) of the slices that the lanes hold; returns this lane's
@@ -182,8 +216,7 @@ __device__ __forceinline__ void wave_argmax(float& m, int& at) {
 __device__ __forceinline__ double join(bool mine, double m, double z, double* m_out, double* z_out) {
     const bool some = mine && z > 0.0;
     double top = some ? m : -1e300;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = __builtin_fmax(top, __shfl_xor(top, d));
+    reduce_steps([&](auto d) { top = __builtin_fmax(top, from_lane<d.value>(top)); });
     if (top == -1e300) top = 0.0;
     const double s = some ? shift_to(z, m, top) : 0.0;
     *m_out = top;
@@ -208,6 +241,7 @@ struct Shared {
     int wave_i[NWAVES];
     double bcast[8];
     int ibcast[8];
+    double scan[kGroup][NWAVES];
     int gone[SV_MAX_DRAFT];  // one-hot: the rejected siblings' tokens and their p
     double gone_p[SV_MAX_DRAFT];
     int n_gone;
@@ -284,7 +318,7 @@ __device__ void slice_argmax(const T* row, int64_t lo, int64_t hi, bool vec, Sha
 // (M, sum of 2^(l c2 - M)) of a slice, M the power of its maximum, in one
 // sweep: a thread sums against its own power, raised once per group of tiles.
 template <typename T>
-__device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, double c2, Shared& sh, double* m_out,
+__device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, const Scale& scale, Shared& sh, double* m_out,
                             double* z_out) {
     constexpr int GROUP = kGroup / sizeof(T);
     float top = -__builtin_inff();
@@ -301,11 +335,11 @@ __device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, doub
             for (int j = 0; j < kPer; ++j) top = fmaxf(top, x[j]);
         }
         if (top > was) {
-            const double mn = power_of(top, c2);
+            const double mn = power_of(top, scale.c2);
             z = was == -__builtin_inff() ? 0.0 : shift_to(z, m, mn);
             m = mn;
         }
-        const Power power(sh.pow2, c2, m);
+        const Power power(sh.pow2, scale, m);
 #pragma unroll
         for (int t = 0; t < GROUP; ++t) {
             if (base + t * (NT * kPer) >= hi) continue;  // the whole workgroup at once
@@ -315,7 +349,7 @@ __device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, doub
         }
     }
     const float all = block_max(top, sh.wave_f);
-    const double mc = power_of(all, c2);
+    const double mc = power_of(all, scale.c2);
     z = top == -__builtin_inff() ? 0.0 : shift_to(z, m, mc);
     *z_out = block_sum(z, sh.wave_a);
     *m_out = mc;
@@ -325,8 +359,8 @@ __device__ void slice_stats(const T* row, int64_t lo, int64_t hi, bool vec, doub
 struct Mass {
     Power p, q;
     double iz, tq;
-    __device__ __forceinline__ Mass(const double* pow2, const TreeState& s, double c2)
-        : p(pow2, c2, s.m_t), q(pow2, c2, s.m_q), iz(1.0 / s.z_t), tq(s.t / s.z_q) {}
+    __device__ __forceinline__ Mass(const double* pow2, const TreeState& s, const Scale& c)
+        : p(pow2, c, s.m_t), q(pow2, c, s.m_q), iz(1.0 / s.z_t), tq(s.t / s.z_q) {}
     __device__ __forceinline__ double operator()(float lt, float lq) const {
         return __builtin_fmax(0.0, __builtin_fma(-tq, q(lq), iz * p(lt)));
     }
@@ -334,10 +368,10 @@ struct Mass {
 
 // Sum of max(0, p - t q) over a slice.
 template <typename T>
-__device__ double slice_mass(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, double c2, const TreeState& s,
+__device__ double slice_mass(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, const Scale& scale, const TreeState& s,
                              Shared& sh) {
     constexpr int GROUP = kGroup / sizeof(T) / 2;
-    const Mass mass(sh.pow2, s, c2);
+    const Mass mass(sh.pow2, s, scale);
     double f = 0.0;
     for (int64_t base = lo; base < hi; base += GROUP * NT * kPer) {
         Raw<T> a[GROUP], b[GROUP];
@@ -361,24 +395,22 @@ __device__ double slice_mass(const T* tr, const T* qr, int64_t lo, int64_t hi, b
 
 // The smallest token of [lo, hi) at which the cumulative mass, `run` before lo,
 // passes `goal`; where rounding leaves none, the last one of positive mass (or
-// lo).  Tokens of sh.gone have no mass.
-template <typename T>
-__device__ int slice_draw(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, double c2, const TreeState& s,
+// lo).  Tokens of sh.gone have no mass.  A group of tiles is loaded and scanned
+// at a time; the thread in whose eight tokens the goal lies looks for it there.
+template <typename T, bool PAIR>
+__device__ int slice_draw(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, const Scale& scale, const TreeState& s,
                           double run, double goal, Shared& sh) {
-    const bool pair = qr != nullptr;
-    const Mass mass(sh.pow2, s, c2);
+    constexpr int GROUP = kGroup / sizeof(T) / 2;
+    const Mass mass(sh.pow2, s, scale);
     int last = static_cast<int>(lo);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t base = lo; base < hi; base += NT * kPer) {
-        const int64_t i = base + threadIdx.x * kPer;
+    const auto weights = [&](const Raw<T>& a, const Raw<T>& b, int64_t i, double (&w)[kPer]) {
         float x[kPer], y[kPer];
-        const Raw<T> a = load8(tr, i, hi, vec), b = pair ? load8(qr, i, hi, vec) : a;
         a.get(x);
         b.get(y);
-        double w[kPer], sum = 0.0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            w[j] = pair ? mass(x[j], y[j]) : mass.iz * mass.p(x[j]);
+            w[j] = PAIR ? mass(x[j], y[j]) : mass.iz * mass.p(x[j]);
             if (!(x[j] >= mass.p.low)) w[j] = 0.0;  // logits of -inf are never drawn
         }
         for (int e = 0; e < sh.n_gone; ++e) {
@@ -386,40 +418,80 @@ __device__ int slice_draw(const T* tr, const T* qr, int64_t lo, int64_t hi, bool
 #pragma unroll
             for (int j = 0; j < kPer; ++j) w[j] = d == j ? 0.0 : w[j];
         }
+    };
+    for (int64_t base = lo; base < hi; base += GROUP * NT * kPer) {
+        Raw<T> a[GROUP], b[GROUP];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            sum += w[j];
-            if (w[j] > 0.0) last = static_cast<int>(i + j);
+        for (int t = 0; t < GROUP; ++t) {
+            const int64_t i = base + (t * NT + threadIdx.x) * kPer;
+            a[t] = load8(tr, i, hi, vec);
+            b[t] = PAIR ? load8(qr, i, hi, vec) : a[t];
         }
-        double incl = sum;
+        double sum[GROUP], incl[GROUP];
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double o = __shfl_up(incl, d);
-            if (lane >= d) incl += o;
+        for (int t = 0; t < GROUP; ++t) {
+            const int64_t i = base + (t * NT + threadIdx.x) * kPer;
+            sum[t] = 0.0;
+            if (base + t * (NT * kPer) < hi) {  // the whole workgroup at once
+                double w[kPer];
+                weights(a[t], b[t], i, w);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    sum[t] += w[j];
+                    if (w[j] > 0.0) last = static_cast<int>(i + j);
+                }
+            }
+            incl[t] = sum[t];
         }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+            for (int t = 0; t < GROUP; ++t) {
+                const double o = __shfl_up(incl[t], d);
+                if (lane >= d) incl[t] += o;
+            }
         __syncthreads();
-        if (lane == 63) sh.wave_a[wave] = incl;
+        if (lane == 63)
+#pragma unroll
+            for (int t = 0; t < GROUP; ++t) sh.scan[t][wave] = incl[t];
         if (threadIdx.x == 0) sh.ibcast[0] = INT_MAX;
         __syncthreads();
-        double all = 0.0, before = run + (incl - sum);
+        double before[GROUP];
 #pragma unroll
-        for (int v = 0; v < NWAVES; ++v) {
-            if (v < wave) before += sh.wave_a[v];
-            all += sh.wave_a[v];
-        }
-        int hit = INT_MAX;
-        double c = before;
+        for (int t = 0; t < GROUP; ++t) {
+            before[t] = run + (incl[t] - sum[t]);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            c += w[j];
-            if (hit == INT_MAX && w[j] > 0.0 && c > goal) hit = static_cast<int>(i + j);
+            for (int v = 0; v < NWAVES; ++v) {
+                if (v < wave) before[t] += sh.scan[t][v];
+                run += sh.scan[t][v];
+            }
+            const uint64_t past = __ballot(sum[t] > 0.0 && before[t] + sum[t] > goal);
+            if (past && lane == __builtin_ctzll(past)) atomicMin(&sh.ibcast[0], t * NT + static_cast<int>(threadIdx.x));  // integers: the same whatever the order
         }
-        if (hit != INT_MAX) atomicMin(&sh.ibcast[0], hit);  // integers: the same whatever the order
         __syncthreads();
         const int found = sh.ibcast[0];
-        __syncthreads();
-        if (found != INT_MAX) return found;
-        run += all;
+        if (found != INT_MAX) {
+            if (static_cast<int>(threadIdx.x) == found % NT) {
+#pragma unroll
+                for (int t = 0; t < GROUP; ++t) {
+                    if (t != found / NT) continue;
+                    const int64_t i = base + (t * NT + threadIdx.x) * kPer;
+                    double w[kPer], c = before[t];
+                    weights(a[t], b[t], i, w);
+                    int hit = 0;
+                    bool done = false;
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        c += w[j];
+                        if (!done && w[j] > 0.0) hit = j;
+                        done = done || (w[j] > 0.0 && c > goal);
+                    }
+                    sh.ibcast[3] = static_cast<int>(i) + hit;
+                }
+            }
+            __syncthreads();
+            return sh.ibcast[3];
+        }
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) last = max(last, __shfl_xor(last, d));
@@ -427,6 +499,15 @@ __device__ int slice_draw(const T* tr, const T* qr, int64_t lo, int64_t hi, bool
     __syncthreads();
     for (int v = 0; v < NWAVES; ++v) last = max(last, sh.wave_i[v]);
     return last;
+}
+
+// A token from what is left at the row that `st` stands at.
+template <typename T, int KIND>
+__device__ __forceinline__ int draw_from(const T* target, const T* draft, int64_t lo, int64_t hi, bool vec, const Scale& scale,
+                                         const TreeState& st, double run, double goal, Shared& sh) {
+    if (KIND == kTreeLogits && st.stage == kStageMass)
+        return slice_draw<T, true>(target, draft, lo, hi, vec, scale, st, run, goal, sh);
+    return slice_draw<T, false>(target, target, lo, hi, vec, scale, st, run, goal, sh);
 }
 
 // What lane i knows of node i: read once, ahead of the rows, so that no
@@ -467,7 +548,7 @@ __device__ __forceinline__ Node node_of(const TreePlan& p, int b) {
 // Every workgroup of a sequence may take the decision, one (`lead`) writes it as
 // it is taken; the one that draws writes it again, for `lead` may have left.
 template <int KIND>
-__device__ bool decide(const TreePlan& p, int b, Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
+__device__ __forceinline__ bool decide(const TreePlan& p, int b, Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
     const bool child = (st.left >> lane) & 1;
@@ -479,10 +560,10 @@ __device__ bool decide(const TreePlan& p, int b, Node& node, TreeState& st, int 
     } else {
         double px = 0.0, qx = 0.0;
         if (child) {
-            const Power pt(sh.pow2, p.c2, st.m_t);
+            const Power pt(sh.pow2, Scale(p), st.m_t);
             px = node.l < pt.low ? 0.0 : pt(node.l) / st.z_t;
             if (KIND == kTreeLogits) {
-                const Power pq(sh.pow2, p.c2, st.m_q);
+                const Power pq(sh.pow2, Scale(p), st.m_q);
                 qx = node.d < pq.low ? 0.0 : pq(node.d) / st.z_q;
             }
         }
@@ -686,7 +767,7 @@ __device__ __forceinline__ void join_rows(const TreePlan& p, int b, Shared& sh) 
 // p.row_part the statistics of every row are there already, and only a
 // residual's mass needs another pass.  st is what the next pass works on.
 template <typename T, int KIND>
-__device__ Next go_on(const TreePlan& p, int b, Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
+__device__ __forceinline__ Next go_on(const TreePlan& p, int b, Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
     int slices = p.slices;
     int64_t per = p.per;
@@ -759,8 +840,8 @@ __device__ void draw_token(const TreePlan& p, int b, const Node& node, const Tre
     int y = nx.best;
     if (KIND != kTreeGreedy) {
         const Rows<T, KIND> rows(p, b, st);
-        y = slice_draw(rows.target, st.stage == kStageMass ? rows.draft : static_cast<const T*>(nullptr), nx.from,
-                       min(static_cast<int64_t>(p.vocab), nx.from + nx.len), p.vec != 0, p.c2, st, nx.run, nx.goal, sh);
+        y = draw_from<T, KIND>(rows.target, rows.draft, nx.from, min(static_cast<int64_t>(p.vocab), nx.from + nx.len),
+                               p.vec != 0, Scale(p), st, nx.run, nx.goal, sh);
     }
     if (threadIdx.x < 64) finish(p, b, node, st, y);
 }
@@ -768,7 +849,7 @@ __device__ void draw_token(const TreePlan& p, int b, const Node& node, const Tre
 // The statistics of every row of the tree at once; the last workgroup of a
 // sequence then walks on.
 template <typename T, int KIND>
-__global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
+__global__ __launch_bounds__(NT, KIND == kTreeLogits ? 4 : 1) void k_tree_rows(TreePlan p) {
     __shared__ Shared sh;
     const int slice = blockIdx.x, row = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int64_t V = p.vocab, lo = slice * p.row_per, hi = min(V, lo + p.row_per);
@@ -799,7 +880,7 @@ __global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
             r[0] = m;
             r[1] = where;
         } else {
-            slice_stats(x, lo, hi, p.vec != 0, p.c2, sh, &r[0], &r[1]);
+            slice_stats(x, lo, hi, p.vec != 0, Scale(p), sh, &r[0], &r[1]);
         }
     }
     if (tid == 0)
@@ -904,12 +985,14 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
         if (KIND == kTreeGreedy) {
             slice_argmax(rows.target, lo, hi, vec, sh, &best_m, &best_at);
         } else if (st.stage == kStageRow) {
-            slice_stats(rows.target, lo, hi, vec, p.c2, sh, &r[0], &r[1]);
-            if (rows.draft) slice_stats(rows.draft, lo, hi, vec, p.c2, sh, &r[2], &r[3]);
+            slice_stats(rows.target, lo, hi, vec, Scale(p), sh, &r[0], &r[1]);
+            if (rows.draft) slice_stats(rows.draft, lo, hi, vec, Scale(p), sh, &r[2], &r[3]);
         } else {
-            r[0] = slice_mass(rows.target, rows.draft, lo, hi, vec, p.c2, st, sh);
+            r[0] = slice_mass(rows.target, rows.draft, lo, hi, vec, Scale(p), st, sh);
         }
         if (tid < 64) {
+            // Everything else of the sequence waits for this.
+            __builtin_amdgcn_s_setprio(3);
             // Two sets of words in turn: a workgroup is at most one pass ahead
             // of the slowest, which still reads the other set.
             uint64_t* const set = words + (pass & 1) * 4;
@@ -943,7 +1026,6 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
                 __builtin_amdgcn_s_sleep(1);
             }
             Next nx{false, 0, 0, 0, 0.0, 0.0};
-            const TreeState before = st;
             if (here) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[i] = __longlong_as_double(static_cast<long long>(w[i] & ~uint64_t{255}));
@@ -958,8 +1040,9 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
                 sh.nx = nx;
                 sh.ibcast[1] = here;
                 // what the walk goes on from, should this pass or the draw not be ended here
-                if (lead && (!here || nx.draw)) p.state[b] = here ? st : before;
+                if (lead && (!here || nx.draw)) p.state[b] = st;
             }
+            __builtin_amdgcn_s_setprio(0);
         }
         __syncthreads();
         if (!sh.ibcast[1]) return;
@@ -1016,10 +1099,10 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
             float m;
             slice_argmax(rows.target, 0, V, vec, sh, &m, &best);
         } else if (st.stage == kStageRow) {
-            slice_stats(rows.target, 0, V, vec, p.c2, sh, &st.m_t, &st.z_t);
-            if (rows.draft) slice_stats(rows.draft, 0, V, vec, p.c2, sh, &st.m_q, &st.z_q);
+            slice_stats(rows.target, 0, V, vec, Scale(p), sh, &st.m_t, &st.z_t);
+            if (rows.draft) slice_stats(rows.draft, 0, V, vec, Scale(p), sh, &st.m_q, &st.z_q);
         } else {
-            st.f = slice_mass(rows.target, rows.draft, 0, V, vec, p.c2, st, sh);
+            st.f = slice_mass(rows.target, rows.draft, 0, V, vec, Scale(p), st, sh);
         }
         __syncthreads();
         if (threadIdx.x < 64) {
@@ -1036,8 +1119,7 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
         if (KIND != kTreeGreedy) {
             const double all = st.stage == kStageMass ? st.f : 1.0 - gone_mass(sh, 0, V);
             const double u = p.uniforms[static_cast<int64_t>(b) * (p.k + 1) + p.k];
-            y = slice_draw(rows.target, st.stage == kStageMass ? rows.draft : static_cast<const T*>(nullptr), 0, V, vec,
-                           p.c2, st, 0.0, u * all, sh);
+            y = draw_from<T, KIND>(rows.target, rows.draft, 0, V, vec, Scale(p), st, 0.0, u * all, sh);
         }
         if (threadIdx.x < 64) finish(p, b, node, st, y);
         return;
