@@ -68,20 +68,18 @@ constexpr int kTreeThreads = 256;
 constexpr int kTreeMaxSlices = 64;
 constexpr int kTreeMaxBatch = 65535;
 constexpr int kTreeWgs = 1024;   // workgroups of a walk's pass: as many as run at once
-// Workgroups that read every row at once, about: what runs at once, and twice
-// that where draft rows are among them, of which those of leaves are not read.
-// 8 x 17 rows of 151936: 39 us with 1024, 42 with 1536, 44 with 2048; with a
-// drafter's rows 89, 79 and 72.
+// Workgroups that read every row at once, about: as many as run at once.  8 x 17
+// rows of 151936: 39 us with 1024, 42 with 1536, 44 with 2048.
 constexpr int kTreeRowWgs = 1024;
-constexpr int kTreeRowWgsLogits = 2048;
 constexpr int kTreeDies = 8;
 constexpr uint64_t kTreeWaitTicks = 2000000;  // of 10 ns: how long a workgroup waits for the others of its sequence
 constexpr int kTreeTile = kTreeThreads * 8;  // tokens one workgroup takes at a time
-// Logits up to which every row is read at once.  At 41 Mi logits (B = 16, k = 16,
-// V = 151936) that takes 59 us for one-hot children against 66 row by row, and
-// 24 against 52 for greedy walks, which read twice as fast; at 10 Mi 18 against 45.
-constexpr int64_t kTreeAllRows = int64_t{48} << 20;
-constexpr int64_t kTreeAllRowsGreedy = int64_t{96} << 20;
+// Logits up to which every row is read at once (one-hot children, and greedy
+// walks, which read twice as fast): rows of 151936, k = 16, 8 sequences (20 Mi)
+// take 35 us at once against 41 row by row, 16 take 62 against 41; greedy walks
+// of 16 (39 Mi) 25 against 36, of 32 (79 Mi) 43 against 40.
+constexpr int64_t kTreeAllRows = int64_t{24} << 20;
+constexpr int64_t kTreeAllRowsGreedy = int64_t{64} << 20;
 
 enum TreeKind : int32_t { kTreeGreedy = 0, kTreeOneHot = 1, kTreeLogits = 2 };
 
@@ -112,7 +110,7 @@ struct TreePlan {
     uint64_t* exchange;          // [kTreeWgs][2][4]: partials of a walk's passes, tagged
     // Written by a call before it is read:
     TreeState* state;            // [B]
-    double* row_part;            // [B][k+1+draft_rows][kTreeMaxSlices][2]: every row's, or NULL (rows read as the walk comes to them)
+    double* row_part;            // [B][k+1][kTreeMaxSlices][2]: every row's, or NULL (rows read as the walk comes to them)
     int64_t per, row_per;        // tokens of one slice: of a pass, and where every row is read at once
     int32_t slices, row_slices;  // workgroups on one row
     int32_t batch, k, vocab, draft_rows;

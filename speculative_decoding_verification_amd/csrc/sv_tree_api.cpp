@@ -106,8 +106,7 @@ sv_status plan_tree(const sv_verify_tree_desc* d, TreePlan* p) {
     p->c2 = t == 0.f ? 0.0 : kLog2E / static_cast<double>(t);
     p->per_c2 = t == 0.f ? 0.0 : static_cast<double>(t) / kLog2E;
     tree_slices(p->vocab, p->batch, kTreeWgs, &p->per, &p->slices);
-    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1 + p->draft_rows),
-                p->kind == kTreeLogits ? kTreeRowWgsLogits : kTreeRowWgs, &p->row_per, &p->row_slices);
+    tree_slices(p->vocab, static_cast<int64_t>(p->batch) * (p->k + 1), kTreeRowWgs, &p->row_per, &p->row_slices);
     p->wait_ticks = tree_wait_ticks;
     return SV_OK;
 }
@@ -123,13 +122,13 @@ constexpr size_t kTreeZeroBytes = 2 * kTreeCountBytes + kTreeExchangeBytes;
 // Whether the statistics of every row are taken at once.
 bool all_rows(const TreePlan& p) {
     const int64_t most = p.kind == kTreeGreedy ? kTreeAllRowsGreedy : kTreeAllRows;
-    return p.slices > 1 && static_cast<int64_t>(p.batch) * (p.k + 1 + p.draft_rows) * p.vocab <= most;
+    return p.kind != kTreeLogits && p.slices > 1 && static_cast<int64_t>(p.batch) * (p.k + 1) * p.vocab <= most;
 }
 
 size_t tree_bytes(const TreePlan& p) {
     size_t n = kTreeZeroBytes + tree_state_bytes(p.batch);
     if (all_rows(p))
-        n += align_up(static_cast<size_t>(p.batch) * (p.k + 1 + p.draft_rows) * kTreeMaxSlices * 2 * sizeof(double));
+        n += align_up(static_cast<size_t>(p.batch) * (p.k + 1) * kTreeMaxSlices * 2 * sizeof(double));
     return n;
 }
 

@@ -245,7 +245,7 @@ struct Shared {
     int gone[SV_MAX_DRAFT];  // one-hot: the rejected siblings' tokens and their p
     double gone_p[SV_MAX_DRAFT];
     int n_gone;
-    double row_m[2 * SV_MAX_DRAFT + 2], row_z[2 * SV_MAX_DRAFT + 2];  // every row's statistics: join_rows
+    double row_m[SV_MAX_DRAFT + 1], row_z[SV_MAX_DRAFT + 1];  // every row's statistics: join_rows
     TreeState st;
     Next nx;
 };
@@ -400,7 +400,7 @@ __device__ double slice_mass(const T* tr, const T* qr, int64_t lo, int64_t hi, b
 template <typename T, bool PAIR>
 __device__ int slice_draw(const T* tr, const T* qr, int64_t lo, int64_t hi, bool vec, const Scale& scale, const TreeState& s,
                           double run, double goal, Shared& sh) {
-    constexpr int GROUP = kGroup / sizeof(T) / 2;
+    constexpr int GROUP = PAIR ? 1 : kGroup / sizeof(T) / 2;  // more are spilled
     const Mass mass(sh.pow2, s, scale);
     int last = static_cast<int>(lo);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -516,14 +516,13 @@ struct Node {
     int up, tok;
     double u;
     float l, d;  // the logits of its token in its parent's target and draft row
-    int kept;    // not of node i: the i-th node that this workgroup saw kept, or -1
 };
 
 template <typename T, int KIND>
 __device__ __forceinline__ Node node_of(const TreePlan& p, int b) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
-    Node n{-2, -1, 0.0, 0.f, 0.f, -1};
+    Node n{-2, -1, 0.0, 0.f, 0.f};
     if (lane < p.k) {
         n.up = p.parents[bk + lane];
         n.tok = p.tokens[bk + lane];
@@ -545,10 +544,9 @@ __device__ __forceinline__ Node node_of(const TreePlan& p, int b) {
 // The walk's next decision, taken by the first wavefront.  On entry st holds
 // the row's statistics (or F(t)); on return its stage says what is needed next,
 // and the answer is true when a token is to be drawn from what is left at st.at.
-// Every workgroup of a sequence may take the decision, one (`lead`) writes it as
-// it is taken; the one that draws writes it again, for `lead` may have left.
+// Every workgroup of a sequence may take the decision, one (`lead`) writes it.
 template <int KIND>
-__device__ __forceinline__ bool decide(const TreePlan& p, int b, Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
+__device__ __forceinline__ bool decide(const TreePlan& p, int b, const Node& node, TreeState& st, int argmax, bool lead, Shared& sh) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
     const bool child = (st.left >> lane) & 1;
@@ -608,7 +606,6 @@ __device__ __forceinline__ bool decide(const TreePlan& p, int b, Node& node, Tre
             p.path[bk + st.kept] = hit;
             p.out_tokens[bk + b + st.kept] = x;
         }
-        if (lane == st.kept) node.kept = hit;
         st.kept += 1;
         st.at = hit;
         st.left = __ballot(node.up == hit);
@@ -650,14 +647,9 @@ __device__ void refuse(const TreePlan& p, int b) {
     }
 }
 
-__device__ void finish(const TreePlan& p, int b, const Node& node, const TreeState& st, int token) {
+__device__ void finish(const TreePlan& p, int b, const TreeState& st, int token) {
     const int lane = threadIdx.x & 63;
     const int64_t bk = static_cast<int64_t>(b) * p.k;
-    const int x = __shfl(node.tok, max(node.kept, 0));
-    if (node.kept >= 0 && lane < st.kept) {
-        p.path[bk + lane] = node.kept;
-        p.out_tokens[bk + b + lane] = x;
-    }
     if (lane == 0) {
         p.accepted_len[b] = st.kept;
         p.out_tokens[bk + b + st.kept] = token;
@@ -727,12 +719,11 @@ __device__ __forceinline__ bool fits(const TreePlan& p, int b, const Node& node,
 // wavefront, by the others: several rows to a wavefront, a lane to a slice.
 template <int KIND>
 __device__ __forceinline__ void join_rows(const TreePlan& p, int b, Shared& sh) {
-    const int rows = p.k + 1 + p.draft_rows;
     int width = 1;
     while (width < p.row_slices) width <<= 1;
     const int i = threadIdx.x & (width - 1);
-    for (int row = (threadIdx.x - 64) / width; row < rows; row += (NT - 64) / width) {
-        const double* const part = p.row_part + ((static_cast<int64_t>(b) * rows + row) * kTreeMaxSlices + i) * 2;
+    for (int row = (threadIdx.x - 64) / width; row <= p.k; row += (NT - 64) / width) {
+        const double* const part = p.row_part + ((static_cast<int64_t>(b) * (p.k + 1) + row) * kTreeMaxSlices + i) * 2;
         double m = 0.0, z = 0.0;
         if (i < p.row_slices) {
             m = taken(part);
@@ -762,117 +753,121 @@ __device__ __forceinline__ void join_rows(const TreePlan& p, int b, Shared& sh) 
     }
 }
 
-// Goes on with a walk whose pass is complete, as far as what is known reaches
-// (the first wavefront).  r: the pass's partials, lane i's of slice i.  With
-// p.row_part the statistics of every row are there already, and only a
-// residual's mass needs another pass.  st is what the next pass works on.
-template <typename T, int KIND>
-__device__ __forceinline__ Next go_on(const TreePlan& p, int b, Node& node, TreeState& st, double (&r)[4], bool lead, Shared& sh) {
+// Where the token lies that is to be drawn, by the mass of each lane's slice
+// (the first wavefront).
+template <int KIND>
+__device__ __forceinline__ void place(const TreePlan& p, int b, double mass, int slices, int64_t per, const Shared& sh,
+                                      Next& nx) {
     const int lane = threadIdx.x & 63;
-    int slices = p.slices;
-    int64_t per = p.per;
+    if (KIND == kTreeOneHot) mass = __builtin_fmax(0.0, mass - gone_mass(sh, lane * per, (lane + 1) * per));
+    if (lane >= slices) mass = 0.0;
+    double cum = mass;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(cum, d);
+        if (lane >= d) cum += o;
+    }
+    nx.goal = static_cast<double>(p.uniforms[static_cast<int64_t>(b) * (p.k + 1) + p.k]) * __shfl(cum, 63);
+    uint64_t past = __ballot(mass > 0.0 && cum > nx.goal);
+    if (!past) {  // rounding left none: the last slice that holds anything
+        const uint64_t any = __ballot(mass > 0.0);
+        past = any ? uint64_t{1} << (63 - __builtin_clzll(any)) : 1;
+    }
+    const int at = __builtin_ctzll(past);
+    nx.run = __shfl(cum - mass, at);
+    nx.from = at * per;
+    nx.len = per;
+}
+
+// Goes on with a walk whose pass is complete, by one decision (the first
+// wavefront).  r: the pass's partials, lane i's of slice i.  st is what the next
+// pass works on.
+template <int KIND>
+__device__ __forceinline__ Next go_on(const TreePlan& p, int b, const Node& node, TreeState& st, const double (&r)[4],
+                                      bool lead, Shared& sh) {
+    const bool mine = static_cast<int>(threadIdx.x & 63) < p.slices;
     Next nx{false, 0, 0, 0, 0.0, 0.0};
     double mass = 0.0;  // of this lane's slice
-    while (true) {
-        const bool by_rows = p.row_part && st.stage == kStageRow;
-        if (by_rows) {
-            slices = p.row_slices;
-            per = p.row_per;
-        }
-        if (KIND == kTreeGreedy && by_rows) {
+    if (KIND == kTreeGreedy) {
+        float m = mine ? static_cast<float>(r[0]) : -__builtin_inff();
+        nx.best = mine ? static_cast<int>(r[1]) : INT_MAX;
+        wave_argmax(m, nx.best);
+    } else if (st.stage == kStageRow) {
+        mass = join(mine, r[0], r[1], &st.m_t, &st.z_t) / st.z_t;
+        if (KIND == kTreeLogits && st.left) join(mine, r[2], r[3], &st.m_q, &st.z_q);
+    } else {
+        mass = mine ? r[0] : 0.0;
+        st.f = wave_sum(mass);
+    }
+    nx.draw = decide<KIND>(p, b, node, st, nx.best, lead, sh);
+    if (nx.draw && KIND != kTreeGreedy) place<KIND>(p, b, mass, p.slices, p.per, sh, nx);
+    return nx;
+}
+
+// The whole walk, every row's statistics being there (the first wavefront).
+template <int KIND>
+__device__ __forceinline__ Next walk_rows(const TreePlan& p, int b, const Node& node, TreeState& st, Shared& sh) {
+    const int lane = threadIdx.x & 63;
+    Next nx{false, 0, 0, 0, 0.0, 0.0};
+    while (!nx.draw) {
+        if (KIND == kTreeGreedy) {
             nx.best = static_cast<int>(sh.row_z[st.at + 1]);
-        } else if (KIND == kTreeGreedy) {
-            float m = lane < slices ? static_cast<float>(r[0]) : -__builtin_inff();
-            nx.best = lane < slices ? static_cast<int>(r[1]) : INT_MAX;
-            wave_argmax(m, nx.best);
-        } else if (by_rows) {
+        } else {
             st.m_t = sh.row_m[st.at + 1];
             st.z_t = sh.row_z[st.at + 1];
-            if (KIND == kTreeLogits && st.left) {
-                st.m_q = sh.row_m[p.k + 1 + st.at + 1];
-                st.z_q = sh.row_z[p.k + 1 + st.at + 1];
-            }
-        } else if (st.stage == kStageRow) {
-            mass = join(lane < slices, r[0], r[1], &st.m_t, &st.z_t) / st.z_t;
-            if (KIND == kTreeLogits && st.left) join(lane < slices, r[2], r[3], &st.m_q, &st.z_q);
-        } else {
-            mass = lane < slices ? r[0] : 0.0;
-            st.f = wave_sum(mass);
         }
-        nx.draw = decide<KIND>(p, b, node, st, nx.best, lead, sh);
-        if (nx.draw || !p.row_part || st.stage != kStageRow) break;
+        nx.draw = decide<KIND>(p, b, node, st, nx.best, true, sh);
     }
-    if (nx.draw && KIND != kTreeGreedy) {
-        if (p.row_part && st.stage == kStageRow) {
-            const int64_t row = static_cast<int64_t>(b) * (p.k + 1 + p.draft_rows) + st.at + 1;
-            const double* const part = p.row_part + (row * kTreeMaxSlices + lane) * 2;
-            if (lane < slices) {
-                r[0] = taken(part);
-                r[1] = taken(part + 1);
-            }
-            mass = lane < slices && r[1] > 0.0 ? shift_to(r[1], r[0], st.m_t) / st.z_t : 0.0;
+    if (KIND == kTreeOneHot) {
+        const int64_t row = static_cast<int64_t>(b) * (p.k + 1) + st.at + 1;
+        const double* const part = p.row_part + (row * kTreeMaxSlices + lane) * 2;
+        double m = 0.0, z = 0.0;
+        if (lane < p.row_slices) {
+            m = taken(part);
+            z = taken(part + 1);
         }
-        if (KIND == kTreeOneHot) mass = __builtin_fmax(0.0, mass - gone_mass(sh, lane * per, (lane + 1) * per));
-        if (lane >= slices) mass = 0.0;
-        double cum = mass;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double o = __shfl_up(cum, d);
-            if (lane >= d) cum += o;
-        }
-        nx.goal = static_cast<double>(p.uniforms[static_cast<int64_t>(b) * (p.k + 1) + p.k]) * __shfl(cum, 63);
-        uint64_t past = __ballot(mass > 0.0 && cum > nx.goal);
-        if (!past) {  // rounding left none: the last slice that holds anything
-            const uint64_t any = __ballot(mass > 0.0);
-            past = any ? uint64_t{1} << (63 - __builtin_clzll(any)) : 1;
-        }
-        const int at = __builtin_ctzll(past);
-        nx.run = __shfl(cum - mass, at);
-        nx.from = at * per;
-        nx.len = per;
+        place<KIND>(p, b, z > 0.0 ? shift_to(z, m, st.m_t) / st.z_t : 0.0, p.row_slices, p.row_per, sh, nx);
     }
     return nx;
 }
 
 // The token that is due, and the sequence's end (the whole workgroup).
 template <typename T, int KIND>
-__device__ void draw_token(const TreePlan& p, int b, const Node& node, const TreeState& st, const Next& nx, Shared& sh) {
+__device__ void draw_token(const TreePlan& p, int b, const TreeState& st, const Next& nx, Shared& sh) {
     int y = nx.best;
     if (KIND != kTreeGreedy) {
         const Rows<T, KIND> rows(p, b, st);
         y = draw_from<T, KIND>(rows.target, rows.draft, nx.from, min(static_cast<int64_t>(p.vocab), nx.from + nx.len),
                                p.vec != 0, Scale(p), st, nx.run, nx.goal, sh);
     }
-    if (threadIdx.x < 64) finish(p, b, node, st, y);
+    if (threadIdx.x < 64) finish(p, b, st, y);
 }
 
 // The statistics of every row of the tree at once; the last workgroup of a
-// sequence then walks on.
+// sequence then takes the walk.  Not for children from a draft row: there a
+// rejection asks for another pass over its rows, and walks of the cluster's
+// kind were faster from 1 sequence (53 against 72 us, k = 16, V = 151936) to 64
+// (101 against 285).
 template <typename T, int KIND>
-__global__ __launch_bounds__(NT, KIND == kTreeLogits ? 4 : 1) void k_tree_rows(TreePlan p) {
+__global__ __launch_bounds__(NT) void k_tree_rows(TreePlan p) {
+    static_assert(KIND != kTreeLogits);
     __shared__ Shared sh;
     const int slice = blockIdx.x, row = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int64_t V = p.vocab, lo = slice * p.row_per, hi = min(V, lo + p.row_per);
-    const int target_rows = p.k + 1, rows = target_rows + p.draft_rows;
-    const bool target = row < target_rows;
-    const int at = target ? row - 1 : row - target_rows - 1;  // the node whose row it is
     if (tid < 64) {
-        // rows of absent nodes, and draft rows that nothing was drawn from, are not read
+        // rows of absent nodes are not read
         const int up = tid < p.k ? p.parents[static_cast<int64_t>(b) * p.k + tid] : -2;
-        const bool wanted = at < 0 || __shfl(up, max(at, 0)) != -2;
-        const bool used = target || __ballot(up == at) != 0;
+        const bool wanted = row == 0 || __shfl(up, max(row - 1, 0)) != -2;
         if (KIND != kTreeGreedy) sh.pow2[tid] = pow2_entry(tid);
         if (tid == 0) {
-            sh.ibcast[0] = wanted && used;
+            sh.ibcast[0] = wanted;
             sh.n_gone = 0;
         }
     }
     __syncthreads();
     double r[4] = {0.0, 0.0, 0.0, 0.0};
     if (sh.ibcast[0]) {
-        const T* const x = target ? static_cast<const T*>(p.target) + (static_cast<int64_t>(b) * target_rows + row) * V
-                                  : static_cast<const T*>(p.draft) +
-                                        (static_cast<int64_t>(b) * p.draft_rows + row - target_rows) * V;
+        const T* const x = static_cast<const T*>(p.target) + (static_cast<int64_t>(b) * (p.k + 1) + row) * V;
         if (KIND == kTreeGreedy) {
             float m;
             int where;
@@ -884,36 +879,31 @@ __global__ __launch_bounds__(NT, KIND == kTreeLogits ? 4 : 1) void k_tree_rows(T
         }
     }
     if (tid == 0)
-        sh.ibcast[2] = hand_in(p.row_part + ((static_cast<int64_t>(b) * rows + row) * kTreeMaxSlices + slice) * 2, r, 2,
-                               &p.arrived[b], static_cast<uint32_t>(p.row_slices) * rows);
+        sh.ibcast[2] =
+            hand_in(p.row_part + ((static_cast<int64_t>(b) * (p.k + 1) + row) * kTreeMaxSlices + slice) * 2, r, 2,
+                    &p.arrived[b], static_cast<uint32_t>(p.row_slices) * (p.k + 1));
     __syncthreads();
     if (!sh.ibcast[2]) return;
     Node node{};
-    TreeState st{};
     if (tid < 64) node = node_of<T, KIND>(p, b);
     else join_rows<KIND>(p, b, sh);
     __syncthreads();
     if (tid < 64) {
+        TreeState st{};
         begin<KIND>(p, b, node, st);
         Next nx{false, 0, 0, 0, 0.0, 0.0};
         if (st.stage == kStageDone) refuse(p, b);
-        else nx = go_on<T, KIND>(p, b, node, st, r, true, sh);
+        else nx = walk_rows<KIND>(p, b, node, st, sh);
         if (tid == 0) {
             sh.st = st;
             sh.nx = nx;
+            p.arrived[b] = 0;
         }
     }
     __syncthreads();
-    st = sh.st;
+    const TreeState st = sh.st;
     const Next nx = sh.nx;
-    if (nx.draw) draw_token<T, KIND>(p, b, node, st, nx, sh);
-    if (tid == 0) {
-        p.arrived[b] = 0;
-        if (KIND == kTreeLogits) {  // the kernels that follow go on with it
-            p.state[b] = st;
-            p.finished[b] = nx.draw || st.stage == kStageDone;
-        }
-    }
+    if (nx.draw) draw_token<T, KIND>(p, b, st, nx, sh);
 }
 
 // A value handed to the other workgroups: its low byte (2^-44 of it) is the
@@ -933,42 +923,27 @@ __device__ __forceinline__ uint64_t tagged(double x, uint32_t pass) {
 // gives up leaves, the first one leaves the state behind, and k_tree_walk ends
 // the walk from there.
 template <typename T, int KIND>
-__global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
+__global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p) {
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 63;
     const int die = blockIdx.x % kTreeDies, on_die = blockIdx.x / kTreeDies;
     const int b = on_die / p.slices * kTreeDies + die, slice = on_die % p.slices;
     if (b >= p.batch) return;
-    if (!first && p.finished[b]) return;
     const bool lead = slice == 0;
     TreeState st{};
-    if (first) {  // at the root; whether it has children is seen later
-        st.at = -1;
-        st.left = KIND == kTreeLogits;
-        st.stage = kStageRow;
-    } else {
-        st = p.state[b];
-        if (!in_range<KIND>(p, st)) return;
-    }
     Node node{};
     if (tid < 64) {
         if (KIND != kTreeGreedy) sh.pow2[tid] = pow2_entry(tid);
         node = node_of<T, KIND>(p, b);
-        if (first) {
-            begin<KIND>(p, b, node, st);
-            if (st.stage == kStageDone && lead) {
-                refuse(p, b);
-                if (tid == 0) p.finished[b] = 1;
-            }
-        } else if (!fits<KIND>(p, b, node, st)) {
-            st.stage = kStageDone;
+        begin<KIND>(p, b, node, st);
+        if (st.stage == kStageDone && lead) {
+            refuse(p, b);
+            if (tid == 0) p.finished[b] = 1;
         }
         if (tid == 0) {
             sh.st = st;
             sh.n_gone = 0;
         }
-    } else if (p.row_part) {
-        join_rows<KIND>(p, b, sh);
     }
     const int64_t V = p.vocab, lo = slice * p.per, hi = min(V, lo + p.per);
     const bool vec = p.vec != 0;
@@ -1033,7 +1008,7 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
                     r[0] = __uint_as_float(static_cast<uint32_t>(w[0] >> 32));
                     r[1] = static_cast<double>((w[0] >> 8) & 0xFFFFFF);
                 }
-                nx = go_on<T, KIND>(p, b, node, st, r, lead, sh);
+                nx = go_on<KIND>(p, b, node, st, r, lead, sh);
             }
             if (tid == 0) {
                 sh.st = st;
@@ -1051,7 +1026,7 @@ __global__ __launch_bounds__(NT, 4) void k_tree_cluster(TreePlan p, int first) {
             const bool mine = KIND == kTreeGreedy ? lead : slice == nx.from / p.per;
             if (mine) {
                 st = sh.st;
-                draw_token<T, KIND>(p, b, node, st, nx, sh);
+                draw_token<T, KIND>(p, b, st, nx, sh);
                 if (tid == 0) p.finished[b] = 1;
             }
             return;
@@ -1121,7 +1096,7 @@ __global__ __launch_bounds__(NT) void k_tree_walk(TreePlan p, int first) {
             const double u = p.uniforms[static_cast<int64_t>(b) * (p.k + 1) + p.k];
             y = draw_from<T, KIND>(rows.target, rows.draft, 0, V, vec, Scale(p), st, 0.0, u * all, sh);
         }
-        if (threadIdx.x < 64) finish(p, b, node, st, y);
+        if (threadIdx.x < 64) finish(p, b, st, y);
         return;
     }
 }
@@ -1132,13 +1107,14 @@ hipError_t launch_kind(const TreePlan& p, hipStream_t stream) {
         k_tree_walk<T, KIND><<<p.batch, NT, 0, stream>>>(p, 1);
         return hipGetLastError();
     }
-    if (p.row_part) {
-        k_tree_rows<T, KIND><<<dim3(p.row_slices, p.k + 1 + p.draft_rows, p.batch), NT, 0, stream>>>(p);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || KIND != kTreeLogits) return e;
+    if constexpr (KIND != kTreeLogits) {
+        if (p.row_part) {
+            k_tree_rows<T, KIND><<<dim3(p.row_slices, p.k + 1, p.batch), NT, 0, stream>>>(p);
+            return hipGetLastError();
+        }
     }
     const int blocks = (p.batch + kTreeDies - 1) / kTreeDies * kTreeDies * p.slices;
-    k_tree_cluster<T, KIND><<<blocks, NT, 0, stream>>>(p, !p.row_part);
+    k_tree_cluster<T, KIND><<<blocks, NT, 0, stream>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_tree_walk<T, KIND><<<p.batch, NT, 0, stream>>>(p, 0);
