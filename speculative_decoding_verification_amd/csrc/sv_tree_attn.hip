@@ -9,17 +9,24 @@
 // disjoint key ranges join exactly as l = sum_i l_i 2^{m_i - m}.
 //
 //  k_tree_attn     Work is cut into key tiles of 32 keys per wavefront.  A unit
-//                  is one (sequence, key head, block of up to 64 query rows);
-//                  the tiles of all units stand in one line, and each of
-//                  kAttnWgs workgroups takes an equal run of it, whatever the
-//                  lengths of the sequences are: a single long sequence is
-//                  spread over the device and a ragged batch stays balanced,
-//                  with no host knowledge of the lengths.  Within a workgroup
-//                  the wavefronts take turns at 32-key steps, each with all of
-//                  the unit's rows, so a wavefront's keys and values pass
-//                  through LDS of its own and the loop holds no barrier.
+//                  is one (sequence, key head, block of up to 64 query rows),
+//                  the units of one key head a cluster; the tiles of all key
+//                  heads stand in one line, and each cluster takes an equal run
+//                  of it, whatever the lengths of the sequences are: a single
+//                  long sequence is spread over the device and a ragged batch
+//                  stays balanced, with no host knowledge of the lengths.  512
+//                  workgroups run, two to a compute unit, so that one's loads go
+//                  on while the other starts or ends a run; the workgroups of a
+//                  cluster read the same keys at the same time on one die, so
+//                  that its L2 gives all but the first their keys.  Within a
+//                  workgroup the wavefronts take turns at 32-key steps, each
+//                  with all of the unit's rows, so a wavefront's keys and values
+//                  pass through LDS of its own and the loop holds no barrier.
 //                  K and V rows go from memory straight to LDS
-//                  (global_load_lds_dwordx4), two steps deep.  Scores are
+//                  (global_load_lds_dwordx4): K of the step after the next and V
+//                  of the next are in flight while a step is computed, and page
+//                  numbers go the same way (a load of one into a register makes
+//                  the compiler wait for every load in flight).  Scores are
 //                  formed transposed, S^T = K Q^T (v_mfma_f32_16x16x32), so a
 //                  lane holds keys of one query row: maxima and sums need two
 //                  lane exchanges, and the weights are in the operand layout of
@@ -30,11 +37,26 @@
 //                  the 16-bit operand, whose relative rounding is the same), so
 //                  most steps neither exchange lanes nor rescale.
 //                  Weights are rounded to the cache's 16-bit type for the
-//                  matrix product, relative 2^-9 (bf16) or 2^-12 (f16) each;
-//                  sums, maxima and products are 32-bit.
-//  k_tree_combine  Joins the partial results of units that several workgroups
-//                  share, in workgroup order (no atomics: reproducible), and
-//                  writes the zeros of absent sequences.
+//                  matrix product, by at most 2^-8 (bf16) or 2^-11 (f16) of
+//                  themselves; sums, maxima and products are 32-bit.
+//  k_tree_combine  Joins the partial results of units that several clusters
+//                  share, in their order (no atomics: reproducible), and writes
+//                  the zeros of absent sequences.
+//
+// What bounds it.  (k + 1) q_heads / kv_heads rows use each key: up to about 100
+// rows memory does, beyond that the matrix cores.  Measured, both kernels
+// (bf16 unless said, head size 128, 8 key heads):
+//   1 sequence of 1000 keys, 4 rows a key head   9 + 4 us: launches, and two
+//     trips to memory (the run, its pages) before the first key
+//   64 x 2.9 K keys, 32 rows   142 + 10 us; its 709 MB take 101 us at the
+//     7.0 TB/s of a plain read.  6.5 TB/s inside a run; its start (finding the
+//     run 2 us, the first loads 2.5 us), its end and the combine are the rest
+//   16 x 11 K keys, 520 rows, f16   640 + 16 us, 570 TFLOP/s of the 1330 that a
+//     library product of 8192^3 reaches: a step's softmax (one exponential, two
+//     multiply-adds and a conversion a score) takes as many cycles as its
+//     matrix instructions and only partly runs beside them.  Units of 64 rows,
+//     not fewer: 638 us against 734 with 48 and 1059 with 32, since each unit
+//     reads the keys from the L2 again.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
