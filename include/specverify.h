@@ -652,8 +652,14 @@ size_t sv_verify_tree_workspace_bytes(const sv_verify_tree_desc* desc);
  *                 other entry points; calls that use the same workspace must
  *                 not overlap in time.
  *
- * Probabilities and sums are 64-bit.  NaN logits and rows that are all -inf
- * give unspecified (but in-bounds) results.
+ * Probabilities and sums are 64-bit, a probability good to 1e-11 of itself; a
+ * residual whose mass is below that of p or q (a child that was not drawn from
+ * its draft row can leave one) is not told from rounding.  |l / T| is to be
+ * below 5e12.  NaN logits and rows that are all -inf give unspecified (but
+ * in-bounds) results.
+ * A sequence's workgroups wait for each other for at most 20 ms; a walk that
+ * was not ended then is ended, with the same result, by a kernel that runs on
+ * one workgroup a sequence.
  * Errors (nothing launched): SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE,
  * SV_ERR_BAD_DTYPE, SV_ERR_BAD_TEMPERATURE, SV_ERR_BAD_DRAFT_KIND,
  * SV_ERR_MISALIGNED, SV_ERR_WORKSPACE_TOO_SMALL.  Launch failure: SV_ERR_HIP.

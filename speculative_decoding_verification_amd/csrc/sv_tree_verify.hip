@@ -25,7 +25,25 @@
 // parts of a row join by exact shifts, and the rounding to the power, the
 // exponent's bias and M are one constant: see Power.
 //
-// Only the rows on the walked path are read.
+// Kernels.  k_tree_cluster takes the walks row by row and reads only the rows on
+// the walked path, several workgroups to a sequence, on one die, which hand each
+// other a pass's partials and all take the same decision.  k_tree_rows reads
+// every row of the trees at once instead, where there are few (kTreeAllRows):
+// it reads more and waits less.  k_tree_walk is one workgroup a sequence: the
+// whole walk of a small vocabulary, and the end of a walk whose workgroups did
+// not wait for each other long enough.
+//
+// What bounds them (V = 151936, bf16, k = 16).  128 sequences with a drafter's
+// rows: 151 us, 3.4 passes over two rows on average and up to 6; the 264 MB that
+// have to be read take 38 us at 7.0 TB/s and the logits' 2^x, 12 operations
+// each, about 65 us.  A pass of all sequences takes about 21 us of that
+// arithmetic, 6 of waiting for the slowest workgroup of a sequence, 1.6 of the
+// decision; the rest is sequences that walk longer than others.  64 with
+// one-hot children 56 us, 64 greedy walks 46 us.  8 with one-hot children, all
+// 41 MB of rows at once, 35 us: 6 of reading, 8 of 2^x, then the walk, the draw
+// within a slice, and the launch.  4 sequences of 1000 tokens 15 us, one
+// workgroup each: four or five trips to memory one after the other.
+// Workgroups of 256: 512 took 213 us where 256 take 188 and 128 take 203.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -684,9 +702,8 @@ __device__ __forceinline__ double gone_mass(const Shared& sh, int64_t lo, int64_
 
 // Hands four words to the workgroup that arrives last: agent-scope stores
 // reach memory past this die's L2, the wait sees them arrive, and only then is
-// the arrival counted, so no cache is written back or invalidated (a release
-// fence here cost 4 us a pass and more, every workgroup's fence emptying its
-// die's L2).  Called by one thread; true on the last arrival.
+// the arrival counted, so no cache is written back or invalidated.  Called
+// by one thread; true on the last arrival.
 __device__ __forceinline__ bool hand_in(double* part, const double (&r)[4], int n, uint32_t* arrived, uint32_t all) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
