@@ -577,7 +577,8 @@ size_t sv_tree_attention_workspace_bytes(const sv_tree_attention_desc* desc);
  *  page_table     device, [B][max_pages] int32
  *  seq_len        device, [B] int32
  *  parents        device, [B][k] int32 (may be NULL when k == 0)
- *  out            device out, [B][k+1][q_heads][head_dim] dtype, 16-byte aligned
+ *  out            device out, [B][k+1][q_heads][head_dim] dtype, 16-byte
+ *                 aligned; must not overlap q
  *  lse_out        device out or NULL, [B][k+1][q_heads] float32: ln sum e^{s_j}
  *  workspace      device, >= sv_tree_attention_workspace_bytes(desc) bytes,
  *                 16-byte aligned (needs no clearing).  Calls that use the same
@@ -592,7 +593,8 @@ size_t sv_tree_attention_workspace_bytes(const sv_tree_attention_desc* desc);
  * weights are rounded to dtype for the matrix product.
  * Errors (nothing launched): SV_ERR_NULL_ARG, SV_ERR_BAD_SHAPE,
  * SV_ERR_BAD_DTYPE, SV_ERR_BAD_SCALE, SV_ERR_MISALIGNED,
- * SV_ERR_WORKSPACE_TOO_SMALL.  Launch failure: SV_ERR_HIP.
+ * SV_ERR_WORKSPACE_TOO_SMALL, SV_ERR_ALIASED (out == q).  Launch failure:
+ * SV_ERR_HIP.
  */
 sv_status sv_tree_attention(const sv_tree_attention_desc* desc, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* page_table, const int32_t* seq_len,

@@ -187,6 +187,7 @@ sv_status sv_tree_attention(const sv_tree_attention_desc* desc, const void* q, c
         !sv::aligned(workspace, 16))
         return SV_ERR_MISALIGNED;
     if (workspace_bytes < sv::attention_bytes(p)) return SV_ERR_WORKSPACE_TOO_SMALL;
+    if (out == q) return SV_ERR_ALIASED;  // rows are written while workgroups with other keys still read them
     p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;

@@ -73,9 +73,10 @@ def bind(lib) -> None:
 
 
 class _Pool:
-    """Workspaces by (device, stream), grown on demand: calls on one stream run
-    in order and share one, calls on others may overlap.  An outgrown buffer is
-    kept, as work on a stream that torch does not know may still use it.
+    """Workspaces by (device, stream), grown on demand to at least twice the size:
+    calls on one stream run in order and share one, calls on others may overlap.
+    An outgrown buffer is kept, as work on a stream that torch does not know may
+    still use it.
     `zero`: the entry point wants its workspace zero-filled once."""
 
     def __init__(self, zero: bool):
@@ -91,6 +92,7 @@ class _Pool:
         if buf is None or buf.numel() < nbytes:
             if buf is not None:
                 self._old.append(buf)
+                nbytes = max(nbytes, 2 * buf.numel())
             buf = self._buf[(device, stream)] = self.new(device, nbytes)
             if self._make == "zeros" and stream != _stream_of(device, None):
                 _torch().cuda.current_stream(device).synchronize()  # the zeros are there before the other stream looks
@@ -279,7 +281,7 @@ def tree_attention(q, k_cache, v_cache, page_table, seq_len, parents=None, *, sc
     [page_size][head_dim] of q's type, contiguous, the tree's rows appended;
     page_table [B][max_pages], seq_len [B], parents [B][k] int32 (None when k is
     0); scale 1/sqrt(head_dim) by default.  Returns (out, lse or None), out
-    contiguous of q's shape.
+    contiguous of q's shape (given or not, it must not overlap q).
     """
     return TreeAttention(q, k_cache, v_cache, page_table, seq_len, parents, scale=scale, return_lse=return_lse,
                          out=out, workspace=workspace, _pooled=True)()

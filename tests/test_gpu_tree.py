@@ -786,3 +786,38 @@ def test_calls_on_another_stream(dev):
         got = [sv.tree_attention(*a).out, call().out.clone()]
     side.synchronize()
     assert all(torch.equal(want, g) for g in got)
+
+
+def test_prepared_calls_in_two_graphs(dev):
+    """A step's attention and walk captured twice, each with prepared calls of its own, replayed in turn and at once on two
+    streams, with eager calls of other shapes between."""
+    on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
+    walks, attns, want = [], [], []
+    for i in range(2):
+        c = Case(dev, k=5, lens=(300, 17, 900), fill=0.0, seed=i)
+        w = tuple(on(x) for x in logits_case(30 + i, 12, 6, 30000, 1.0, False))
+        attns.append(sv.TreeAttention(*c.args()))
+        walks.append(sv.TreeVerifier(*w, 1.0))
+        want.append([x.clone() for x in (*sv.verify_tree(*w, 1.0), sv.tree_attention(*c.args()).out)])
+        attns[i](), walks[i]()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((*walks[i](), attns[i]().out))
+        graphs.append(g)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(4):
+        for o in outs:
+            for x in o:
+                x.zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(sides[i] if turn % 2 else sides[0]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(x, y) for x, y in zip(outs[i], want[i])), (turn, i)
+        small = tuple(on(x) for x in logits_case(turn, 3, 4, 5000, 1.0, True))
+        sv.verify_tree(*small, 1.0, onehot=True)

@@ -66,6 +66,10 @@ def test_attention_rejects_bad_arguments(lib):
     assert attn_call(lib, empty, **{x: None for x in ("q", "k_cache", "out", "workspace")}) == ST["SV_OK"]
 
 
+def test_attention_rejects_output_on_its_queries(lib):
+    assert attn_call(lib, attn_desc(), out=1 << 20, q=1 << 20) == ST["SV_ERR_ALIASED"]
+
+
 def tree_desc(**over):
     f = dict(B=2, k=5, V=100, draft_rows=4, dtype=sv.SV_BF16, draft_kind=sv.SV_DRAFT_LOGITS, temperature=1.0)
     f.update(over)
