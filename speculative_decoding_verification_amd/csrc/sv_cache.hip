@@ -143,17 +143,18 @@ __global__ __launch_bounds__(kCopyThreads) void k_cache_commit(CommitPlan p) {
 }
 
 // Inclusive sum over the bookkeeping workgroup, and the total.
-__device__ __forceinline__ int book_scan(int v, int* total, int* tmp) {
+template <typename N>
+__device__ __forceinline__ N book_scan(N v, N* total, N* tmp) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
+        const N o = __shfl_up(v, d);
         if (lane >= d) v += o;
     }
     __syncthreads();
     if (lane == 63) tmp[wave] = v;
     __syncthreads();
-    int all = 0;
+    N all = 0;
 #pragma unroll
     for (int w = 0; w < kBookWaves; ++w) {
         if (w < wave) v += tmp[w];
@@ -190,7 +191,10 @@ __device__ __forceinline__ int free_pages(const CachePlan& c, int need, int* tmp
 }
 
 __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, const int32_t* want, int32_t* status) {
-    __shared__ int ends[kCacheMaxSeqs];  // pages asked for by the sequences up to and including this one
+    // Pages asked for by the sequences up to and including this one; together
+    // they may ask for more than 2^31.
+    __shared__ int64_t ends[kCacheMaxSeqs];
+    __shared__ int64_t wide[kBookWaves];
     __shared__ int tmp[kBookWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t page = int64_t{1} << c.page_shift;
@@ -216,25 +220,25 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
         if (lane == 0) c.page_count[b] = static_cast<int>(t);
     }
     settle();
-    int need = 0;
+    int64_t need = 0;
     for (int base = 0; base < c.n_seqs; base += kBookThreads) {
         const int b = base + threadIdx.x;
-        int more = 0;
+        int64_t more = 0;
         if (b < c.n_seqs) {
             const int have = fresh(&c.page_count[b]);
             const int64_t t = target(b, have);
-            more = t > have ? static_cast<int>(t - have) : 0;
+            more = t > have ? t - have : 0;
             if (status) status[b] = t >= 0;
         }
-        int all;
-        const int incl = book_scan(more, &all, tmp);
+        int64_t all;
+        const int64_t incl = book_scan(more, &all, wide);
         if (b < c.n_seqs) ends[b] = need + incl;
         need += all;
     }
     __syncthreads();
     if (need == 0) return;
-    const auto begin_of = [&](int b) { return b ? ends[b - 1] : 0; };
-    const int found = free_pages(c, need, tmp, [&](int rank, int id) {
+    const auto begin_of = [&](int b) -> int64_t { return b ? ends[b - 1] : 0; };
+    const int found = free_pages(c, static_cast<int>(min(need, static_cast<int64_t>(c.n_pages))), tmp, [&](int rank, int id) {
         int lo = 0, hi = c.n_seqs - 1;  // the first sequence whose end is past this rank
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -248,15 +252,15 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
     // Served are the sequences whose whole wish lies before the last free
     // page; the one that it falls into gives its part back.
     for (int b = wave; b < c.n_seqs; b += kBookWaves) {
-        const int lo = begin_of(b), hi = ends[b];
+        const int64_t lo = begin_of(b), hi = ends[b];
         if (lo == hi) continue;
         const int have = fresh(&c.page_count[b]);
         if (hi <= found) {
-            if (lane == 0) c.page_count[b] = have + hi - lo;
+            if (lane == 0) c.page_count[b] = static_cast<int>(have + hi - lo);
             continue;
         }
         int32_t* const row = c.page_table + static_cast<int64_t>(b) * c.max_pages + have;
-        for (int r = lo + lane; r < min(hi, found); r += 64) {
+        for (int64_t r = lo + lane; r < min(hi, static_cast<int64_t>(found)); r += 64) {
             c.page_refs[fresh(&row[r - lo])] = 0;
             row[r - lo] = -1;
         }

@@ -678,6 +678,22 @@ def test_cache_far_offsets(dev):
     assert torch.equal(kc[:, 4197, :, 250:254], kc[:, 4199, :, 250:254]) and torch.equal(vc[1, 4197, 3, 253], vc[1, 4199, 3, 253])
 
 
+def test_resize_wishes_past_32_bits(dev):
+    """Wishes that add up to more than 2^31 pages: the first sequence is served, the others are refused and unchanged."""
+    width, P = 1 << 29, 64
+    table = torch.full((6, width), -1, dtype=torch.int32, device=dev)
+    count, refs = torch.zeros(6, dtype=torch.int32, device=dev), torch.zeros(P, dtype=torch.int32, device=dev)
+    want = torch.tensor([10] + [width] * 4 + [5], dtype=torch.int32, device=dev)
+    status = sv.cache_resize(want, table, count, refs, page_size=1)
+    assert status.tolist() == [1, 0, 0, 0, 0, 0] and count.tolist() == [10, 0, 0, 0, 0, 0]
+    assert refs.tolist() == [1] * 10 + [0] * (P - 10)
+    assert table[:, :80].cpu().tolist() == [list(range(10)) + [-1] * 70] + [[-1] * 80] * 5
+    want[1:] = torch.tensor([width] * 5, dtype=torch.int32, device=dev)  # 10 + 5 * 2^29 passes 2^31
+    status = sv.cache_resize(want, table, count, refs, page_size=1)
+    assert status.tolist() == [1, 0, 0, 0, 0, 0] and count.tolist() == [10, 0, 0, 0, 0, 0]
+    assert refs.tolist() == [1] * 10 + [0] * (P - 10) and (table[1:, :80] == -1).all()
+
+
 def test_empty_batches(dev):
     z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device=dev)  # noqa: E731
     c = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device=dev)
