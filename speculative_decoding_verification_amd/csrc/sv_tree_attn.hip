@@ -52,9 +52,9 @@
 //     7.0 TB/s of a plain read.  6.5 TB/s inside a run; its start (finding the
 //     run 2 us, the first loads 2.5 us), its end and the combine are the rest
 //   16 x 11 K keys, 520 rows, f16   640 + 16 us, 570 TFLOP/s of the 1330 that a
-//     library product of 8192^3 reaches: a step's softmax (one exponential, two
-//     multiply-adds and a conversion a score) takes as many cycles as its
-//     matrix instructions and only partly runs beside them.  Units of 64 rows,
+//     library product of 8192^3 reaches: matrix instructions take 26% of the
+//     cycles, vector instructions, most of them the softmax's, 37%, and a SIMD
+//     has one wavefront, which waits for the rest.  Units of 64 rows,
 //     not fewer: 638 us against 734 with 48 and 1059 with 32, since each unit
 //     reads the keys from the L2 again.
 #include <hip/hip_runtime.h>
