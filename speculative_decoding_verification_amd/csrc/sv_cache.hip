@@ -12,11 +12,12 @@
 // 349 MB in 67 to 72 us, 4.9 to 5.2 TB/s read and written, as fast as a plain
 // copy (4.76).  Moving the accepted rows of 128 sequences in 32 layers, 77 MB in
 // pieces of 256 bytes, takes 24 us (3.2 TB/s).  Copying the 112 begun pages of
-// 16 sequences forked seven times, 32 layers, 1.2 GB, takes 220 us (5.5 TB/s).
-// The bookkeeping is one workgroup's: 5 us a fork of 3 and 3 us a resize, 15 and
-// 13 us with 128 sequences, whose ranks and counts go through its LDS (through
-// memory with a fence each the first took 24 us).  Calls that move less are
-// bound by their launch.
+// 16 sequences forked seven times, 32 layers, 1.2 GB, takes 218 to 250 us by the
+// card (4.8 to 5.5 TB/s).  The bookkeeping is one workgroup's, a thread to a
+// sequence and its ranks and counts in LDS: 5 us a fork of 3 and 4 a resize, 11
+// and 10 with 128 sequences (17 and 15 with a wavefront to a sequence from the
+// start, and 24 a fork of 3 through memory with fences).  Calls that move less
+// are bound by their launch.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -196,6 +197,7 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
     __shared__ int64_t ends[kCacheMaxSeqs];
     __shared__ int64_t wide[kBookWaves];
     __shared__ int tmp[kBookWaves];
+    __shared__ int cut;  // the sequence whose wish the last free page falls into
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t page = int64_t{1} << c.page_shift;
     // A count or a wish that the table cannot hold is refused; the others are
@@ -206,18 +208,26 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
         const int64_t t = w < 0 ? have : (w + page - 1) >> c.page_shift;
         return t > c.max_pages ? -1 : t;
     };
-    // Shorter ones give back the pages behind their new end.
-    for (int b = wave; b < c.n_seqs; b += kBookWaves) {
+    // Shorter ones give back the pages behind their new end.  A thread to a
+    // sequence for what it has and wants, a wavefront to one that gives back.
+    if (threadIdx.x == 0) cut = -1;
+    for (int b = threadIdx.x; b < c.n_seqs; b += kBookThreads) {
         const int have = c.page_count[b];
         const int64_t t = target(b, have);
-        if (t < 0 || t >= have) continue;
+        const bool less = t >= 0 && t < have;
+        ends[b] = less ? static_cast<int64_t>(have) << 32 | t : -1;
+        if (less) c.page_count[b] = static_cast<int>(t);
+    }
+    __syncthreads();
+    for (int b = wave; b < c.n_seqs; b += kBookWaves) {
+        if (ends[b] < 0) continue;
+        const int64_t have = ends[b] >> 32, t = ends[b] & 0xFFFFFFFF;
         int32_t* const row = c.page_table + static_cast<int64_t>(b) * c.max_pages;
         for (int64_t i = t + lane; i < have; i += 64) {
             const int id = row[i];
             if (id >= 0 && id < c.n_pages) atomicSub(&c.page_refs[id], 1);
             row[i] = -1;
         }
-        if (lane == 0) c.page_count[b] = static_cast<int>(t);
     }
     settle();
     int64_t need = 0;
@@ -251,20 +261,22 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_resize(CachePlan c, cons
     settle();
     // Served are the sequences whose whole wish lies before the last free
     // page; the one that it falls into gives its part back.
-    for (int b = wave; b < c.n_seqs; b += kBookWaves) {
+    for (int b = threadIdx.x; b < c.n_seqs; b += kBookThreads) {
         const int64_t lo = begin_of(b), hi = ends[b];
         if (lo == hi) continue;
-        const int have = fresh(&c.page_count[b]);
         if (hi <= found) {
-            if (lane == 0) c.page_count[b] = static_cast<int>(have + hi - lo);
+            c.page_count[b] = static_cast<int>(fresh(&c.page_count[b]) + hi - lo);
             continue;
         }
-        int32_t* const row = c.page_table + static_cast<int64_t>(b) * c.max_pages + have;
-        for (int64_t r = lo + lane; r < min(hi, static_cast<int64_t>(found)); r += 64) {
-            c.page_refs[fresh(&row[r - lo])] = 0;
-            row[r - lo] = -1;
-        }
-        if (lane == 0 && status) status[b] = 0;
+        if (status) status[b] = 0;
+        if (lo < found) cut = b;
+    }
+    __syncthreads();
+    if (cut < 0) return;
+    int32_t* const row = c.page_table + static_cast<int64_t>(cut) * c.max_pages + fresh(&c.page_count[cut]);
+    for (int i = threadIdx.x; i < static_cast<int>(found - begin_of(cut)); i += kBookThreads) {
+        c.page_refs[fresh(&row[i])] = 0;
+        row[i] = -1;
     }
 }
 
@@ -317,30 +329,38 @@ __global__ __launch_bounds__(kBookThreads) void k_cache_fork(ForkPlan p) {
     __syncthreads();
     for (int r = found + threadIdx.x; r < need; r += kBookThreads) new_page[pair_of[r]] = -2;  // none left
     __syncthreads();
-    for (int i = wave; i < p.n; i += kBookWaves) {
+    // A thread to a pair for the counts and the begun page, a wavefront for the
+    // whole pages: what it needs stays where the claims and ranks were.
+    for (int i = threadIdx.x; i < p.n; i += kBookThreads) {
         const int id = new_page[i];
-        if (lane == 0) {
-            p.new_page[i] = id;
-            if (p.status) p.status[i] = id != -2;
+        p.new_page[i] = id;
+        if (p.status) p.status[i] = id != -2;
+        int old = -1, whole = -1;
+        if (id != -2) {
+            const int s = p.src[i], d = p.dst[i], len = c.seq_len[s];
+            whole = len >> c.page_shift;
+            if (id >= 0) {
+                old = c.page_table[static_cast<int64_t>(s) * c.max_pages + whole];
+                c.page_table[static_cast<int64_t>(d) * c.max_pages + whole] = id;
+            }
+            c.page_count[d] = whole + (id >= 0);
+            c.seq_len[d] = len;
+            claim[i] = s;
+            pair_of[i] = d;
         }
-        if (id == -2) {
-            if (lane == 0) p.old_page[i] = -1;
-            continue;
-        }
-        const int s = p.src[i], d = p.dst[i];
-        const int len = c.seq_len[s], whole = len >> c.page_shift;
-        const int32_t* const from = c.page_table + static_cast<int64_t>(s) * c.max_pages;
-        int32_t* const to = c.page_table + static_cast<int64_t>(d) * c.max_pages;
+        p.old_page[i] = old;
+        new_page[i] = whole;
+    }
+    __syncthreads();
+    for (int i = wave; i < p.n; i += kBookWaves) {
+        const int whole = new_page[i];
+        if (whole <= 0) continue;
+        const int32_t* const from = c.page_table + static_cast<int64_t>(claim[i]) * c.max_pages;
+        int32_t* const to = c.page_table + static_cast<int64_t>(pair_of[i]) * c.max_pages;
         for (int q = lane; q < whole; q += 64) {
             const int x = from[q];
             to[q] = x;
             if (x >= 0 && x < c.n_pages) atomicAdd(&c.page_refs[x], 1);
-        }
-        if (lane == 0) {
-            if (id >= 0) to[whole] = id;
-            p.old_page[i] = id >= 0 ? from[whole] : -1;
-            c.page_count[d] = whole + (id >= 0);
-            c.seq_len[d] = len;
         }
     }
 }
