@@ -837,3 +837,20 @@ def test_prepared_calls_in_two_graphs(dev):
             assert all(torch.equal(x, y) for x, y in zip(outs[i], want[i])), (turn, i)
         small = tuple(on(x) for x in logits_case(turn, 3, 4, 5000, 1.0, True))
         sv.verify_tree(*small, 1.0, onehot=True)
+
+
+@pytest.mark.parametrize("onehot", [False, True], ids=["logits", "onehot"])
+def test_walk_of_the_most_sequences(dev, onehot):
+    B, k, V = 65535, 2, 11
+    rs = np.random.RandomState(9)
+    t, d = (torch.from_numpy(rs.randn(B, n, V)).float() for n in (k + 1, k))
+    tok = rs.randint(0, V, (B, k)).astype(np.int32)
+    par = np.tile(np.array([-1, 0], np.int32), (B, 1))
+    u = rs.rand(B, k + 1).astype(np.float32)
+    on = lambda x: (torch.from_numpy(x) if isinstance(x, np.ndarray) else x).to(dev)  # noqa: E731
+    r = [x.cpu().numpy() for x in sv.verify_tree(on(t), on(d), on(tok), on(par), on(u), 0.7, onehot=onehot)]
+    for b in list(range(0, B, 997)) + [B - 1]:
+        *want, margin = ref.walk(t[b].double().numpy(), None if onehot else d[b].double().numpy(), tok[b], par[b],
+                                 u[b].astype(np.float64), float(np.float32(0.7)), onehot)
+        if margin > 1.0:
+            assert [r[0][b], list(r[1][b]), list(r[2][b])] == want, b
